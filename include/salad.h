@@ -474,6 +474,170 @@ int salad_linear_state(const void* k, const void* v, int B, int N, int num_heads
                        float* S_out, float* z_out, void* workspace, size_t workspace_bytes,
                        salad_stream_t stream);
 
+/* Element types of salad_rope, salad_ckpt_pack and salad_ckpt_unpack. */
+typedef enum { SALAD_F32 = 0, SALAD_BF16 = 1, SALAD_F16 = 2 } salad_type;
+
+/*
+ * Rotary positions of q and k, which the layer takes as given.  (The SALAD
+ * pages do not say how positions enter; the rotation is the published rotary
+ * embedding, with up to three position axes as video transformers use it.)
+ * A head's first `rot` features are rot/2 pairs, (i, i + rot/2) or, interleaved,
+ * (2i, 2i + 1).  Pair i of a token at position p of the pair's axis becomes
+ *   y1 = scale (x1 cos(p f_i) - x2 sin(p f_i)),  y2 = scale (x2 cos(p f_i) + x1 sin(p f_i));
+ * features [rot, d) are copied.  inverse != 0 negates the sine: applied to the
+ * gradients of y it gives those of x.
+ *
+ * One tensor of the call: `heads` heads of d features, feature stride 1, the
+ * other strides in elements (>= 0 for x; y's elements may not coincide).  y may
+ * be x itself (same type and strides); other overlaps of a y with an x or y of
+ * the call are refused.
+ */
+typedef struct {
+  const void* x;
+  void* y;
+  int heads;
+  int64_t x_stride_b, x_stride_n, x_stride_h;
+  int64_t y_stride_b, y_stride_n, y_stride_h;
+} salad_rope_tensor;
+/*
+ *   tensors    HOST [count], count 1 or 2 (q and k: one launch, the angles of a
+ *              token are formed once for the heads of both).
+ *   x_type, y_type  salad_type of every x and of every y.
+ *   d          1..512;  rot even, 2 <= rot <= d.
+ *   inv_freq   DEVICE fp64 [rot/2], 8-byte aligned: f_i.
+ *   axis_pairs HOST int32 [axes], axes 1..3: consecutive pairs that follow each
+ *              axis; they sum to rot/2 (0 allowed).
+ *   positions  DEVICE int32 [N][axes] for every sequence, pos_stride_b elements
+ *              apart (0: the same for all), or NULL: token n lies at
+ *              origin + (n / (W H), n / W mod H, n mod W) with grid_h = H, grid_w
+ *              = W (1, 1: one axis counting tokens); any int32 value.
+ *   origin     HOST int32 [3], used when positions is NULL; NULL is (0, 0, 0).
+ *   scale      finite factor of the turned pairs (1, or a long-context factor).
+ * Angles are formed in fp64 and reduced before the fp32 sine and cosine; the
+ * products are fp32 with one rounding to y's type.  Never synchronises, no
+ * workspace.  Errors: INVALID_ARG, UNSUPPORTED (d > 512, more than 2^31 - 1
+ * tokens), CUDA.
+ */
+int salad_rope(const salad_rope_tensor* tensors, int count, int x_type, int y_type, int B, int N, int d, int rot,
+               int interleaved, const double* inv_freq, const int32_t* axis_pairs, int axes,
+               const int32_t* positions, int64_t pos_stride_b, int grid_h, int grid_w, const int32_t* origin,
+               float scale, int inverse, salad_stream_t stream);
+
+/*
+ * Activation checkpoints in 8 bits, for a training step that keeps q, k and v of
+ * every layer (the SALAD summary, section 3, fine-tunes through the layer; at
+ * 75,600 tokens x 40 heads of 128 they are 2.3 GB a layer in bf16).  Every row's
+ * values are taken in groups of 32 (the last may be shorter) that share a
+ * power-of-two scale:
+ *   e    = the smallest exponent >= -127 with max|x| / 2^e <= 127 (SALAD_INT8) or 448 (SALAD_E4M3)
+ *   code = x / 2^e rounded to nearest even;  scale byte = e + 127;  decoded = code 2^e
+ * An int8 code is off by at most half a step, 2^(e-1) <= max|x| / 127; an
+ * e4m3 code by 2^-4 of the value, or 2^(e-10) near 0.  Decoding to bf16 is exact.
+ * A group that holds an infinity or a NaN decodes to NaN (byte 255).  A value
+ * that would round past the output type's largest decodes to the largest.
+ */
+typedef enum { SALAD_INT8 = 0, SALAD_E4M3 = 1 } salad_ckpt_format;
+typedef struct {
+  void* x;         /* DEVICE: the values (read by pack, written by unpack) */
+  int64_t stride;  /* elements from row to row, >= cols */
+  uint8_t* codes;  /* DEVICE [rows][cols] */
+  uint8_t* scales; /* DEVICE [rows][ceil(cols/32)] */
+} salad_ckpt_tensor;
+/*
+ *   tensors  HOST [count], count 1..4, all of rows x cols values of `type`
+ *            (salad_type); `format` a salad_ckpt_format.
+ * Any alignment of the element type; 16-byte aligned rows and cols % 32 == 0
+ * take the wide path.  Never synchronises, no workspace.  Errors: INVALID_ARG,
+ * UNSUPPORTED (2^31 groups or more), CUDA.
+ */
+int salad_ckpt_pack(const salad_ckpt_tensor* tensors, int count, int rows, int cols, int type, int format,
+                    salad_stream_t stream);
+int salad_ckpt_unpack(const salad_ckpt_tensor* tensors, int count, int rows, int cols, int type, int format,
+                      salad_stream_t stream);
+
+/*
+ * The layer's backward pass from an 8-bit checkpoint of q, k and v: decodes them
+ * (to bf16, exactly), runs the forward again for out and the log-sum-exps and
+ * then salad_attn_backward, so the gradients are those of the layer at the
+ * decoded q, k, v.  Neither out nor lse has to be kept.
+ *   q_codes, k_codes, v_codes      DEVICE [B][N][Hh][d], 16-byte aligned
+ *   q_scales, k_scales, v_scales   DEVICE [B][N][Hh][d/32]
+ *   dq, dk, dv  DEVICE bf16 [B][N][Hh][d], 16-byte aligned (fp32 sums, one rounding).
+ *   dw, dgate   DEVICE fp32, as salad_attn_backward.
+ *   workspace   DEVICE, >= salad_ckpt_backward_workspace_bytes, 256-byte aligned,
+ *               status word first (zero it once after allocation).
+ * Other arguments and errors as salad_attn_backward.
+ */
+size_t salad_ckpt_backward_workspace_bytes(int B, int N, int num_heads, int d);
+int salad_attn_backward_ckpt(const uint8_t* q_codes, const uint8_t* q_scales, const uint8_t* k_codes,
+                             const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales, int format,
+                             const void* dout, int B, int N, int num_heads, int d, int block, const int32_t* row_ptr,
+                             const int32_t* col_idx, const int32_t* t_row_ptr, const int32_t* t_col_idx,
+                             int mask_per_bh, const void* w_proj, const float* gate, float softmax_scale, float eps,
+                             void* dq, void* dk, void* dv, float* dw, float* dgate, void* workspace,
+                             size_t workspace_bytes, salad_stream_t stream);
+
+/*
+ * Differential attention over a block mask: a variant of the layer's sparse
+ * branch in which each head's q and k (d wide) hold two halves of d/2 features,
+ * each half has its own softmax map over the kept keys, and the maps' difference
+ * weighs the values:
+ *   p_m,ij = softmax_j(scale q_m,i . k_m,j) over the keys kept for i's block (m = 1, 2)
+ *   out_i  = sum_j (p_1,ij - lam[h] p_2,ij) v_j;   0 where the blocks keep no key
+ * (The SALAD pages do not have it; masks, layouts and rules are the layer's.)
+ *   q, k, v, out  DEVICE bf16 [B][N][Hh][d], 16-byte aligned; d = 64 or 128.
+ *   block         128;  row_ptr, col_idx: rows per head, or per (b, h) when
+ *                 mask_per_bh != 0 (salad_build_block_mask, salad_build_topk_mask).
+ *   lam           DEVICE [Hh], bf16 or fp32 by lam_type (salad_type).
+ *   softmax_scale <= 0 selects 1/sqrt(d/2).
+ *   out2, lse     both NULL, or what the backward needs: out2 DEVICE bf16
+ *                 [B][N][Hh][d] (16-byte aligned) is sum_j p_2,ij v_j, lse DEVICE fp32
+ *                 [2][B][Hh][N] the log-sum-exps of both maps (-inf without keys).
+ *   workspace     DEVICE, >= salad_diff_workspace_bytes(B, N, Hh, d), 256-byte
+ *                 aligned, status word first (zero it once after allocation;
+ *                 read it with salad_check_status).
+ * Outputs may not overlap inputs or each other.  Arithmetic: bf16 tensor-core
+ * products with fp32 accumulation, p rounded to bf16 for its product, fp32
+ * softmax, one rounding of each output.  Never synchronises.  Errors:
+ * INVALID_ARG, UNSUPPORTED (d, block, 2^31 query tiles), WORKSPACE, CUDA.
+ */
+size_t salad_diff_workspace_bytes(int B, int N, int num_heads, int d);
+int salad_diff_forward(const void* q, const void* k, const void* v, int B, int N, int num_heads, int d, int block,
+                       const int32_t* row_ptr, const int32_t* col_idx, int mask_per_bh, const void* lam, int lam_type,
+                       float softmax_scale, void* out, void* out2, float* lse, void* workspace,
+                       size_t workspace_bytes, salad_stream_t stream);
+/*
+ * Its gradients.  With dp_ij = dout_i . v_j, D_2,i = dout_i . out2_i and D_1,i = dout_i .
+ * out_i + lam D_2,i:
+ *   ds_m,ij = p_m,ij (dp_ij - D_m,i)
+ *   dq_1,i = scale sum_j ds_1,ij k_1,j,  dq_2,i = -lam scale sum_j ds_2,ij k_2,j,  dk_m,j likewise over i
+ *   dv_j = sum_i (p_1 - lam p_2)_ij dout_i,   dlam[h] = -sum over b, i, j of p_2,ij dp_ij
+ *   out, out2, lse  from salad_diff_forward with the same inputs; dout DEVICE bf16.
+ *   t_row_ptr, t_col_idx  the transposed mask (as salad_attn_backward_sparse).
+ *   dq, dk, dv  DEVICE bf16 [B][N][Hh][d], 16-byte aligned;  dlam DEVICE [Hh] of lam_type.
+ * Sums are fp32 in a fixed order (deterministic), rounded once.  Other
+ * arguments, workspace and errors as salad_diff_forward.
+ */
+int salad_diff_backward(const void* q, const void* k, const void* v, const void* out, const void* out2,
+                        const void* dout, const float* lse, int B, int N, int num_heads, int d, int block,
+                        const int32_t* row_ptr, const int32_t* col_idx, const int32_t* t_row_ptr,
+                        const int32_t* t_col_idx, int mask_per_bh, const void* lam, int lam_type,
+                        float softmax_scale, void* dq, void* dk, void* dv, void* dlam, void* workspace,
+                        size_t workspace_bytes, salad_stream_t stream);
+/*
+ * Differential attention of a few queries against a cache (one token of a
+ * frame-by-frame generation): query i of sequence b sees keys [0, lens[b]).
+ *   q, out   DEVICE bf16 [B][Nq][Hh][d];  k, v  DEVICE bf16 [B][capacity][Hh][d]; 16-byte aligned.
+ *   lens     DEVICE int32 [B], taken as 0 below 0 and as capacity above it; 0: out is 0.
+ *            Keys and values from lens[b] on are not read.
+ * fp32 arithmetic, one rounding, a fixed order of sums; no workspace.  Meant for
+ * Nq of about four or fewer (the keys are read once per four queries).  Errors:
+ * INVALID_ARG, UNSUPPORTED (d, B*Hh*16 >= 2^31, Nq > 262140), CUDA.
+ */
+int salad_diff_decode(const void* q, const void* k, const void* v, int B, int Nq, int capacity, int num_heads, int d,
+                      const int32_t* lens, const void* lam, int lam_type, float softmax_scale, void* out,
+                      salad_stream_t stream);
+
 /*
  * Synchronises `stream`, then reads and clears the workspace status word.
  * Returns SALAD_ERR_DEVICE_TIMEOUT if a kernel of an earlier call gave up on a

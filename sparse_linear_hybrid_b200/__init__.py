@@ -9,12 +9,17 @@ The entry points mirror ``include/salad.h``:
     mask_num_blocks, build_block_mask, validate_mask, tile_num_blocks, build_tile_mask, build_topk_mask,
     workspace_bytes, attn_forward, attn_forward_lse, attn_forward_heads, attn_forward_tiles, attn_forward_static,
     attn_backward_sparse,
-    attn_backward, gate_forward, linear_state, check_status, set_wait_limit_ns, set_max_ctas, set_phase_events,
+    attn_backward, gate_forward, rope_inv_freq, rope_forward, rope_backward, ckpt_pack, ckpt_unpack,
+    new_ckpt_backward_workspace, attn_backward_ckpt, new_diff_workspace, diff_attn_forward, diff_attn_forward_lse,
+    diff_attn_backward, diff_attn_decode, linear_state, check_status, set_wait_limit_ns, set_max_ctas, set_phase_events,
     status_string
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import dataclasses
+import math
 import os
 
 import numpy as np
@@ -33,6 +38,21 @@ SALAD_ERR_CUDA = -5
 SALAD_ERR_DEVICE_TIMEOUT = -6
 SALAD_ERR_OUT_OF_MEMORY = -7
 SALAD_ERR_BAD_MASK = -8
+
+
+# salad_type and salad_ckpt_format
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_FORMATS = {"int8": 0, "e4m3": 1}
+
+
+class _RopeTensor(ctypes.Structure):
+    _fields_ = ([("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int)]
+                + [(f"{a}_stride_{s}", ctypes.c_int64) for a in "xy" for s in "bnh"])
+
+
+class _CkptTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("stride", ctypes.c_int64), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
 
 
 class SaladError(RuntimeError):
@@ -104,6 +124,24 @@ def lib() -> ctypes.CDLL:
         L.salad_build_topk_mask.restype = i
         L.salad_attn_forward_static.argtypes = [p, p, p, i, i, i, i, i, p, p, p, p, f, f, p, p]
         L.salad_attn_forward_static.restype = i
+        L.salad_rope.argtypes = [p, i, i, i, i, i, i, i, i, p, p, i, p, ctypes.c_int64, i, i, p, f, i, p]
+        L.salad_rope.restype = i
+        for fn in (L.salad_ckpt_pack, L.salad_ckpt_unpack):
+            fn.argtypes = [p, i, i, i, i, i, p]
+            fn.restype = i
+        L.salad_ckpt_backward_workspace_bytes.argtypes = [i, i, i, i]
+        L.salad_ckpt_backward_workspace_bytes.restype = sz
+        L.salad_attn_backward_ckpt.argtypes = ([p] * 6 + [i, p] + [i] * 5 + [p] * 4 + [i, p, p, f, f] + [p] * 6
+                                               + [sz, p])
+        L.salad_attn_backward_ckpt.restype = i
+        L.salad_diff_workspace_bytes.argtypes = [i, i, i, i]
+        L.salad_diff_workspace_bytes.restype = sz
+        L.salad_diff_forward.argtypes = [p] * 3 + [i] * 5 + [p, p, i, p, i, f, p, p, p, p, sz, p]
+        L.salad_diff_forward.restype = i
+        L.salad_diff_backward.argtypes = [p] * 7 + [i] * 5 + [p] * 4 + [i, p, i, f] + [p] * 5 + [sz, p]
+        L.salad_diff_backward.restype = i
+        L.salad_diff_decode.argtypes = [p] * 3 + [i] * 5 + [p, p, i, f, p, p]
+        L.salad_diff_decode.restype = i
         L.salad_linear_state.argtypes = [p, p, i, i, i, i, p, p, p, p, sz, p]
         L.salad_linear_state.restype = i
         L.salad_check_status.argtypes = [p, p]
@@ -500,6 +538,428 @@ def attn_forward_static(q, k, v, row_ptr, col_idx, w_proj, gate, block: int, sof
         _dev_ptr(col_idx, torch.int32, "col_idx"), _dev_ptr(w_proj, torch.bfloat16, "w_proj"),
         _dev_ptr(gate, torch.float32, "gate"), float(softmax_scale), float(eps),
         _dev_ptr(out, torch.bfloat16, "out"), _stream(stream)), "salad_attn_forward_static")
+    return out
+
+
+def _on(*tensors):
+    """(context that makes the tensors' device current, that device); all have to be on one CUDA device."""
+    for t in tensors:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError("the tensors must be CUDA tensors (libsalad has no CPU path)")
+    dev = tensors[0].device
+    for t in tensors:
+        if t.device != dev:
+            raise ValueError(f"the tensors lie on several devices: {dev} and {t.device}")
+    if dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext(), dev
+    return torch.cuda.device(dev), dev
+
+
+def rope_inv_freq(rot: int, base: float = 10000.0, sections=None, scaling: str | None = None, factor: float = 1.0,
+                  original_length: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """(frequencies fp64 CUDA [rot/2], scale) of rotary positions.
+
+    Every axis with n = sections[a] pairs has base^(-j/n), j = 0 ... n-1 (sections
+    sum to rot/2; one axis by default).  Long contexts, `factor` times the trained
+    length: "linear" divides every frequency by it; "ntk" raises the base by
+    factor^(n/(n-1)), so that the slowest pair is divided by it and the fastest
+    kept; "yarn" keeps pairs that turn more than beta_fast times within
+    original_length tokens, divides those below beta_slow turns, blends between,
+    and scales the turned pairs by 0.1 ln(factor) + 1."""
+    sections = [rot // 2] if sections is None else [int(n) for n in sections]
+    if rot < 2 or rot % 2 or min(sections) < 0 or sum(sections) != rot // 2:
+        raise ValueError(f"sections {sections} do not sum to rot / 2 = {rot / 2}")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if not (base > 0 and factor >= 1 and math.isfinite(base) and math.isfinite(factor)):
+        raise ValueError("base must be positive and factor at least 1")
+    if scaling == "yarn" and not (original_length > 0 and beta_fast > beta_slow > 0):
+        raise ValueError("yarn needs original_length > 0 and beta_fast > beta_slow > 0")
+    freq, scale = [], 1.0
+    for n in sections:
+        b = base * factor ** (n / (n - 1)) if scaling == "ntk" and n > 1 else base
+        f = np.float64(b) ** (-np.arange(n, dtype=np.float64) / max(n, 1))
+        if scaling == "linear":
+            f = f / factor
+        elif scaling == "yarn":
+            keep = np.clip((original_length * f / (2 * math.pi) - beta_slow) / (beta_fast - beta_slow), 0, 1)
+            f = f * keep + f / factor * (1 - keep)
+            scale = 0.1 * math.log(factor) + 1.0
+        freq.append(f)
+    device = torch.device("cuda") if device is None else torch.device(device)
+    return torch.from_numpy(np.concatenate(freq)).to(device), scale
+
+
+def _rope(q, k, inv_freq, sections, interleaved, scale, positions, grid, origin, q_out, k_out, out_dtype, inverse,
+          stream):
+    xs = [q] if k is None else [q, k]
+    ctx, _ = _on(*xs, inv_freq, *([] if positions is None else [positions]))
+    B, N, _, d = q.shape
+    ys = [q_out, k_out][:len(xs)]
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    with ctx:
+        arr = (_RopeTensor * len(xs))()
+        for i, x in enumerate(xs):
+            if x.dim() != 4 or (x.shape[0], x.shape[1], x.shape[3]) != (B, N, d):
+                raise ValueError("q and k must be [B, N, heads, d] with the same B, N and d")
+            if x.dtype not in _TYPES or x.dtype != q.dtype:
+                raise TypeError("q and k must share one of fp32, bf16, fp16")
+            if ys[i] is None:
+                ys[i] = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+            y = ys[i]
+            if y.shape != x.shape or y.device != x.device or y.dtype not in _TYPES or y.dtype != ys[0].dtype:
+                raise ValueError("outputs must have their input's shape and device, and one type")
+            if out_dtype is not None and y.dtype != out_dtype:
+                raise TypeError(f"the output is {y.dtype}, not {out_dtype}")
+            if d > 1 and (x.stride(3) != 1 or y.stride(3) != 1):
+                raise ValueError("the features of a head must be contiguous")
+            arr[i] = _RopeTensor(x.data_ptr(), y.data_ptr(), x.shape[2], *x.stride()[:3], *y.stride()[:3])
+        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise TypeError("inv_freq must be a contiguous fp64 vector")
+        rot = 2 * inv_freq.numel()
+        sections = [rot // 2] if sections is None else [int(n) for n in sections]
+        axes = len(sections)
+        pos_ptr, pos_b, gh, gw = None, 0, 1, 1
+        if positions is not None:
+            if grid is not None:
+                raise ValueError("give positions or a grid, not both")
+            if positions.dtype != torch.int32:
+                raise TypeError(f"positions must be int32, got {positions.dtype}")
+            p = positions if axes > 1 else positions.unsqueeze(-1)
+            p = p if p.dim() == 3 else p.unsqueeze(0)
+            if p.dim() != 3 or p.shape[0] not in (1, B) or p.shape[1:] != (N, axes) or not p.is_contiguous():
+                raise ValueError(f"positions must be contiguous [B, N{', axes' if axes > 1 else ''}] or without B")
+            pos_ptr, pos_b = ctypes.c_void_p(p.data_ptr()), (N * axes if p.shape[0] > 1 else 0)
+        elif grid is not None:
+            T, gh, gw = (int(n) for n in grid)
+            if axes != 3 or T * gh * gw != N:
+                raise ValueError(f"a grid needs three sections and {T} * {gh} * {gw} tokens, got {axes} and {N}")
+        elif axes != 1:
+            raise ValueError("several sections need positions or a grid")
+        if N == 0 or B == 0:
+            return ys
+        org = (ctypes.c_int32 * 3)(*(list(origin) + [0, 0, 0])[:3])
+        _check(lib().salad_rope(arr, len(xs), _TYPES[q.dtype], _TYPES[ys[0].dtype], B, N, d, rot,
+                                int(bool(interleaved)), ctypes.c_void_p(inv_freq.data_ptr()),
+                                (ctypes.c_int32 * max(axes, 1))(*sections), axes, pos_ptr, pos_b, gh, gw, org,
+                                float(scale), inverse, _stream(stream)), "salad_rope")
+    return ys
+
+
+def rope_forward(q, k, inv_freq, sections=None, interleaved: bool = False, scale: float = 1.0, positions=None,
+                 grid=None, origin=(0, 0, 0), q_out=None, k_out=None, out_dtype=None, stream=None):
+    """q and k (k may be None) turned by their tokens' positions (see salad_rope): (q_out, k_out).
+
+    q, k: CUDA [B, N, heads, d], fp32, bf16 or fp16, any strides with contiguous
+    features (views of a fused projection); inv_freq fp64 [rot/2] and scale from
+    rope_inv_freq.  Positions: int32 CUDA [B, N] or [N] (with several sections
+    [.., N, axes]), or a grid (T, H, W) in raster order from `origin`, or by
+    default origin[0] + n.  Outputs may be q and k themselves."""
+    ys = _rope(q, k, inv_freq, sections, interleaved, scale, positions, grid, origin, q_out, k_out, out_dtype, 0, stream)
+    return ys[0], (ys[1] if k is not None else None)
+
+
+def rope_backward(dq, dk, inv_freq, sections=None, interleaved: bool = False, scale: float = 1.0, positions=None,
+                  grid=None, origin=(0, 0, 0), dq_out=None, dk_out=None, out_dtype=None, stream=None):
+    """Gradients of rope_forward's q and k from those of its outputs (the turn by
+    the opposite angles); attn_backward's fp32 gradients may be stored as bf16."""
+    ys = _rope(dq, dk, inv_freq, sections, interleaved, scale, positions, grid, origin, dq_out, dk_out, out_dtype, 1,
+               stream)
+    return ys[0], (ys[1] if dk is not None else None)
+
+
+@dataclasses.dataclass
+class Checkpoint:
+    """8-bit codes and scale bytes of one tensor (see salad.h): codes uint8 of the
+    tensor's shape, scales uint8 [..., ceil(C/32)] for its last dimension C."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    fmt: str
+    dtype: torch.dtype
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+def _rows_of(x):
+    """(rows, cols, row stride) of a tensor whose groups run along its last
+    dimension; trailing dimensions that lie one after another are taken as one row
+    where that keeps whole groups."""
+    shape, st = x.shape, x.stride()
+    cols, i = shape[-1], x.dim() - 2
+    if cols > 1 and st[-1] != 1:
+        raise ValueError("the last dimension must be contiguous")
+    while i >= 0 and cols % 32 == 0 and (st[i] == cols or shape[i] == 1) and cols * shape[i] < 1 << 30:
+        cols *= shape[i]
+        i -= 1
+    rows, stride = 1, cols
+    first = True
+    while i >= 0:
+        if shape[i] != 1:
+            if first:
+                stride, first = st[i], False
+            elif st[i] != stride * rows:
+                raise ValueError("the rows must lie at one distance from each other")
+            rows *= shape[i]
+        i -= 1
+    return rows, cols, stride
+
+
+def _ckpt_call(fn, name, xs, cks, fmt, stream):
+    """One launch for tensors of the same layout, else one each."""
+    lay = [_rows_of(x) for x in xs]
+    same = all(y[:2] == lay[0][:2] and x.dtype == xs[0].dtype for x, y in zip(xs, lay)) and len(xs) <= 4
+    for part in ([range(len(xs))] if same else [[i] for i in range(len(xs))]):
+        arr = (_CkptTensor * len(part))(*(
+            _CkptTensor(xs[i].data_ptr(), lay[i][2], cks[i].codes.data_ptr(), cks[i].scales.data_ptr()) for i in part))
+        rows, cols, _ = lay[part[0]]
+        if rows and cols:
+            _check(fn(arr, len(part), rows, cols, _TYPES[xs[part[0]].dtype], _FORMATS[fmt], _stream(stream)), name)
+
+
+def _ckpt_scales_shape(shape):
+    return (*shape[:-1], (shape[-1] + 31) // 32)
+
+
+def ckpt_pack(x, fmt: str = "int8", out=None, stream=None):
+    """8-bit checkpoint of a CUDA tensor (fp32, bf16 or fp16), or of each of a list
+    of them (one launch where their layouts agree): groups of 32 along the last
+    dimension share a power-of-two scale (see salad_ckpt_pack).  Rows may lie
+    apart (a view of a fused projection).  fmt "int8" or "e4m3"; `out` reuses
+    earlier checkpoints' memory."""
+    if fmt not in _FORMATS:
+        raise ValueError(f"unknown format {fmt!r}")
+    xs = list(x) if isinstance(x, (list, tuple)) else [x]
+    outs = [None] * len(xs) if out is None else list(out) if isinstance(out, (list, tuple)) else [out]
+    if not xs or len(outs) != len(xs):
+        raise ValueError("one output for each tensor")
+    for t in xs:
+        if not isinstance(t, torch.Tensor) or t.dtype not in _TYPES or t.dim() < 1:
+            raise TypeError("tensors of fp32, bf16 or fp16 with one dimension at least")
+    ctx, dev = _on(*xs)
+    with ctx:
+        for i, t in enumerate(xs):
+            if outs[i] is None:
+                outs[i] = Checkpoint(torch.empty(t.shape, dtype=torch.uint8, device=dev),
+                                     torch.empty(_ckpt_scales_shape(t.shape), dtype=torch.uint8, device=dev), fmt, t.dtype)
+            c = outs[i]
+            if c.codes.shape != t.shape or c.scales.shape != _ckpt_scales_shape(t.shape):
+                raise ValueError("the checkpoint's memory has another shape")
+            _dev_ptr(c.codes, torch.uint8, "codes"), _dev_ptr(c.scales, torch.uint8, "scales"), _on(t, c.codes, c.scales)
+            c.fmt, c.dtype = fmt, t.dtype
+        live = [i for i, t in enumerate(xs) if t.numel()]
+        if live:
+            _ckpt_call(lib().salad_ckpt_pack, "salad_ckpt_pack", [xs[i] for i in live], [outs[i] for i in live], fmt, stream)
+    return outs if isinstance(x, (list, tuple)) else outs[0]
+
+
+def ckpt_unpack(ckpt, dtype=None, out=None, stream=None):
+    """The values of a Checkpoint, or of each of a list, in `dtype` (by default the
+    packed tensor's); exact for bf16 and fp32."""
+    cks = list(ckpt) if isinstance(ckpt, (list, tuple)) else [ckpt]
+    outs = [None] * len(cks) if out is None else list(out) if isinstance(out, (list, tuple)) else [out]
+    if not cks or len(outs) != len(cks):
+        raise ValueError("one output for each checkpoint")
+    if any(c.fmt != cks[0].fmt or c.fmt not in _FORMATS for c in cks):
+        raise ValueError("the checkpoints have several formats")
+    ctx, dev = _on(*(c.codes for c in cks), *(c.scales for c in cks))
+    with ctx:
+        for i, c in enumerate(cks):
+            _dev_ptr(c.codes, torch.uint8, "codes"), _dev_ptr(c.scales, torch.uint8, "scales")
+            if c.scales.shape != _ckpt_scales_shape(c.codes.shape):
+                raise ValueError("scales and codes have shapes that do not agree")
+            if outs[i] is None:
+                outs[i] = torch.empty(c.codes.shape, dtype=dtype or c.dtype, device=dev)
+            if outs[i].shape != c.codes.shape or outs[i].device != dev:
+                raise ValueError("the output has another shape or device")
+            if outs[i].dtype not in _TYPES or (dtype is not None and outs[i].dtype != dtype):
+                raise TypeError("outputs of fp32, bf16 or fp16, as asked for")
+        live = [i for i, c in enumerate(cks) if c.codes.numel()]
+        if live:
+            _ckpt_call(lib().salad_ckpt_unpack, "salad_ckpt_unpack", [outs[i] for i in live], [cks[i] for i in live],
+                       cks[0].fmt, stream)
+    return outs if isinstance(ckpt, (list, tuple)) else outs[0]
+
+
+def new_ckpt_backward_workspace(B: int, N: int, heads: int, d: int, device=None) -> torch.Tensor:
+    """A zero-filled workspace for attn_backward_ckpt."""
+    n = lib().salad_ckpt_backward_workspace_bytes(B, N, heads, d)
+    if n == 0:
+        raise SaladError(SALAD_ERR_INVALID_ARG, "salad_ckpt_backward_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=torch.device("cuda") if device is None else torch.device(device))
+
+
+def attn_backward_ckpt(q, k, v, dout, row_ptr, col_idx, w_proj, gate, block: int = 128, t_row_ptr=None,
+                       t_col_idx=None, softmax_scale: float = 0.0, eps: float = 1e-6, mask_per_bh: bool = False,
+                       workspace=None, stream=None):
+    """The whole layer's gradients from 8-bit checkpoints of q, k and v
+    (ckpt_pack of [B, N, Hh, d] tensors): out and lse are computed again from the
+    decoded values.  A dict of CUDA tensors: dq, dk, dv bf16 [B, N, Hh, d], dw fp32
+    [d, d], dgate fp32 [B, Hh]; the other arguments as attn_backward."""
+    if not (q.fmt == k.fmt == v.fmt) or not (q.codes.shape == k.codes.shape == v.codes.shape) or q.codes.dim() != 4:
+        raise ValueError("checkpoints of q, k and v: one format, one shape [B, N, Hh, d]")
+    B, N, Hh, d = q.codes.shape
+    for c in (q, k, v):
+        if c.scales.shape != _ckpt_scales_shape(c.codes.shape):
+            raise ValueError("scales and codes have shapes that do not agree")
+    if dout.shape != q.codes.shape or w_proj.shape != (d, d) or gate.shape != (B, Hh):
+        raise ValueError("dout, w_proj or gate has another shape than the checkpoints ask for")
+    ctx, dev = _on(q.codes, q.scales, k.codes, k.scales, v.codes, v.scales, dout, row_ptr, col_idx, w_proj, gate)
+    with ctx:
+        nb = (N + block - 1) // block
+        if row_ptr.numel() != (B * Hh if mask_per_bh else Hh) * nb + 1:
+            raise ValueError(f"row_ptr has {row_ptr.numel()} entries, not {(B * Hh if mask_per_bh else Hh) * nb + 1}")
+        t_row_ptr, t_col_idx = _transposed_mask(row_ptr, col_idx, t_row_ptr, t_col_idx,
+                                                mask_per_bh and col_idx.numel(), B * Hh, nb)
+        if t_row_ptr.shape != row_ptr.shape:
+            raise ValueError("the transposed mask has another number of rows")
+        res = {n: torch.empty(B, N, Hh, d, dtype=torch.bfloat16, device=dev) for n in ("dq", "dk", "dv")}
+        res["dw"] = torch.empty(d, d, dtype=torch.float32, device=dev)
+        res["dgate"] = torch.empty(B, Hh, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = new_ckpt_backward_workspace(B, N, Hh, d, dev)
+        u8 = lambda t, name: _dev_ptr(t, torch.uint8, name)  # noqa: E731
+        i32 = lambda t, name: _dev_ptr(t, torch.int32, name)  # noqa: E731
+        _check(lib().salad_attn_backward_ckpt(
+            u8(q.codes, "q.codes"), u8(q.scales, "q.scales"), u8(k.codes, "k.codes"), u8(k.scales, "k.scales"),
+            u8(v.codes, "v.codes"), u8(v.scales, "v.scales"), _FORMATS[q.fmt], _dev_ptr(dout, torch.bfloat16, "dout"),
+            B, N, Hh, d, int(block), i32(row_ptr, "row_ptr"), _cols(col_idx, row_ptr), i32(t_row_ptr, "t_row_ptr"),
+            _cols(t_col_idx, t_row_ptr), int(bool(mask_per_bh)), _dev_ptr(w_proj, torch.bfloat16, "w_proj"),
+            _dev_ptr(gate, torch.float32, "gate"), float(softmax_scale), float(eps),
+            *[_dev_ptr(res[n], torch.bfloat16, n) for n in ("dq", "dk", "dv")],
+            *[_dev_ptr(res[n], torch.float32, n) for n in ("dw", "dgate")],
+            u8(workspace, "workspace"), workspace.numel(), _stream(stream)), "salad_attn_backward_ckpt")
+    return res
+
+
+def new_diff_workspace(B: int, N: int, heads: int, d: int, device=None) -> torch.Tensor:
+    """A zero-filled workspace for the forward and backward of differential attention."""
+    n = lib().salad_diff_workspace_bytes(B, N, heads, d)
+    if n == 0:
+        raise SaladError(SALAD_ERR_INVALID_ARG, "salad_diff_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=torch.device("cuda") if device is None else torch.device(device))
+
+
+def _bf16_like(q, *named):
+    for t, name in named:
+        if t.shape != q.shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(q.shape)}")
+    return [_dev_ptr(t, torch.bfloat16, name) for t, name in named]
+
+
+def _lam(lam, heads):
+    if lam.shape != (heads,):
+        raise ValueError(f"lam has shape {tuple(lam.shape)}, not ({heads},)")
+    if lam.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"lam must be fp32 or bf16, got {lam.dtype}")
+    return _dev_ptr(lam, lam.dtype, "lam"), _TYPES[lam.dtype]
+
+
+def _cols(col_idx, row_ptr):
+    """The column list's pointer; a mask that keeps nothing has none, and none is read."""
+    p = _dev_ptr(col_idx, torch.int32, "col_idx")
+    return p if col_idx.numel() else _dev_ptr(row_ptr, torch.int32, "row_ptr")
+
+
+def _mask_rows(row_ptr, B, N, heads, mask_per_bh):
+    rows = (B * heads if mask_per_bh else heads) * ((N + 127) // 128)
+    if row_ptr.numel() != rows + 1:
+        raise ValueError(f"row_ptr has {row_ptr.numel()} entries, not {rows + 1}")
+
+
+def _diff_forward(q, k, v, row_ptr, col_idx, lam, softmax_scale, mask_per_bh, out, out2, lse, train, workspace, stream):
+    ctx, dev = _on(q, k, v, row_ptr, col_idx, lam)
+    with ctx:
+        B, N, Hh, d = q.shape
+        _mask_rows(row_ptr, B, N, Hh, mask_per_bh)
+        if out is None:
+            out = torch.empty_like(q)
+        if train:
+            out2 = torch.empty_like(q) if out2 is None else out2
+            lse = torch.empty(2, B, Hh, N, dtype=torch.float32, device=dev) if lse is None else lse
+            if lse.shape != (2, B, Hh, N):
+                raise ValueError(f"lse has shape {tuple(lse.shape)}, not {(2, B, Hh, N)}")
+        if workspace is None:
+            workspace = new_diff_workspace(B, N, Hh, d, dev)
+        _on(q, out, workspace, *([out2, lse] if train else []))
+        ptrs = _bf16_like(q, (q, "q"), (k, "k"), (v, "v"), (out, "out"), *([(out2, "out2")] if train else []))
+        _check(lib().salad_diff_forward(
+            *ptrs[:3], B, N, Hh, d, 128, _dev_ptr(row_ptr, torch.int32, "row_ptr"), _cols(col_idx, row_ptr), int(bool(mask_per_bh)), *_lam(lam, Hh), float(softmax_scale),
+            ptrs[3], ptrs[4] if train else None, _dev_ptr(lse, torch.float32, "lse") if train else None,
+            _dev_ptr(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)), "salad_diff_forward")
+    return out, out2, lse
+
+
+def diff_attn_forward(q, k, v, row_ptr, col_idx, lam, softmax_scale: float = 0.0, mask_per_bh: bool = False, out=None,
+                      workspace=None, stream=None) -> torch.Tensor:
+    """Differential attention over a mask of 128-token blocks (see salad_diff_forward):
+    out = (softmax(q_1 k_1^T) - lam softmax(q_2 k_2^T)) v with q_1, k_1 the first and
+    q_2, k_2 the second half of each head's features.
+
+    q, k, v: bf16 CUDA [B, N, Hh, d]; lam fp32 or bf16 [Hh]; mask rows per head, or
+    per (b, h) with mask_per_bh; softmax_scale 0 is 1/sqrt(d/2)."""
+    return _diff_forward(q, k, v, row_ptr, col_idx, lam, softmax_scale, mask_per_bh, out, None, None, False, workspace,
+                         stream)[0]
+
+
+def diff_attn_forward_lse(q, k, v, row_ptr, col_idx, lam, softmax_scale: float = 0.0, mask_per_bh: bool = False,
+                          out=None, out2=None, lse=None, workspace=None, stream=None):
+    """diff_attn_forward that also returns what diff_attn_backward needs: (out, out2,
+    lse) with out2 bf16 [B, N, Hh, d] the second map's output and lse fp32 [2, B, Hh, N]."""
+    return _diff_forward(q, k, v, row_ptr, col_idx, lam, softmax_scale, mask_per_bh, out, out2, lse, True, workspace,
+                         stream)
+
+
+def diff_attn_backward(q, k, v, out, out2, dout, lse, row_ptr, col_idx, lam, t_row_ptr=None, t_col_idx=None,
+                       softmax_scale: float = 0.0, mask_per_bh: bool = False, workspace=None, stream=None):
+    """Gradients of differential attention (see salad_diff_backward): dict of dq, dk,
+    dv bf16 [B, N, Hh, d] and dlam [Hh] of lam's type.  out, out2 and lse come from
+    diff_attn_forward_lse on the same inputs; the transposed mask as in attn_backward_sparse."""
+    ctx, dev = _on(q, k, v, out, out2, dout, lse, row_ptr, col_idx, lam)
+    with ctx:
+        B, N, Hh, d = q.shape
+        _mask_rows(row_ptr, B, N, Hh, mask_per_bh)
+        t_row_ptr, t_col_idx = _transposed_mask(row_ptr, col_idx, t_row_ptr, t_col_idx,
+                                                mask_per_bh and col_idx.numel(), B * Hh, (N + 127) // 128)
+        _mask_rows(t_row_ptr, B, N, Hh, mask_per_bh)
+        if lse.shape != (2, B, Hh, N):
+            raise ValueError(f"lse has shape {tuple(lse.shape)}, not {(2, B, Hh, N)}")
+        res = {n: torch.empty_like(q) for n in ("dq", "dk", "dv")}
+        res["dlam"] = torch.empty_like(lam)
+        if workspace is None:
+            workspace = new_diff_workspace(B, N, Hh, d, dev)
+        _on(q, t_row_ptr, t_col_idx, workspace)
+        ptrs = _bf16_like(q, (q, "q"), (k, "k"), (v, "v"), (out, "out"), (out2, "out2"), (dout, "dout"))
+        i32 = lambda t, name: _dev_ptr(t, torch.int32, name)  # noqa: E731
+        _check(lib().salad_diff_backward(
+            *ptrs, _dev_ptr(lse, torch.float32, "lse"), B, N, Hh, d, 128, i32(row_ptr, "row_ptr"),
+            _cols(col_idx, row_ptr), i32(t_row_ptr, "t_row_ptr"), _cols(t_col_idx, t_row_ptr), int(bool(mask_per_bh)),
+            *_lam(lam, Hh), float(softmax_scale), *[_dev_ptr(res[n], torch.bfloat16, n) for n in ("dq", "dk", "dv")],
+            ctypes.c_void_p(res["dlam"].data_ptr()), _dev_ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
+            _stream(stream)), "salad_diff_backward")
+    return res
+
+
+def diff_attn_decode(q, k_cache, v_cache, lens, lam, softmax_scale: float = 0.0, out=None, stream=None) -> torch.Tensor:
+    """Differential attention of a few queries against a cache (see salad_diff_decode):
+    q bf16 [B, Nq, Hh, d], k_cache and v_cache bf16 [B, capacity, Hh, d], lens int32
+    CUDA [B]; every query of sequence b sees keys [0, lens[b])."""
+    ctx, _ = _on(q, k_cache, v_cache, lens, lam)
+    with ctx:
+        B, Nq, Hh, d = q.shape
+        cap = k_cache.shape[1]
+        if k_cache.shape != (B, cap, Hh, d) or v_cache.shape != k_cache.shape or lens.shape != (B,):
+            raise ValueError("k_cache, v_cache [B, capacity, Hh, d] and lens [B] must fit q")
+        if out is None:
+            out = torch.empty_like(q)
+        _on(q, out)
+        ptrs = _bf16_like(q, (q, "q"), (out, "out"))
+        _check(lib().salad_diff_decode(
+            ptrs[0], _dev_ptr(k_cache, torch.bfloat16, "k_cache"), _dev_ptr(v_cache, torch.bfloat16, "v_cache"), B, Nq,
+            cap, Hh, d, _dev_ptr(lens, torch.int32, "lens"), *_lam(lam, Hh), float(softmax_scale), ptrs[1],
+            _stream(stream)), "salad_diff_decode")
     return out
 
 

@@ -775,6 +775,456 @@ int salad_linear_state(const void* k, const void* v, int B, int N, int num_heads
   return run_linear(k, v, B, N, num_heads, d, gate, nullptr, S_out, z_out, ws, L, s);
 }
 
+}  // extern "C"
+
+namespace {
+
+size_t type_bytes(int type) { return type == SALAD_F32 ? 4 : 2; }
+bool known_type(int type) { return type == SALAD_F32 || type == SALAD_BF16 || type == SALAD_F16; }
+
+// The extent of a [B][N][heads][d] view in elements, and whether its elements
+// are all different (each stride covers the extent of the shorter ones).
+bool view_extent(int B, int N, int heads, int d, const int64_t (&stride)[3], bool distinct, int64_t* extent) {
+  const int size[3] = {B, N, heads};
+  int64_t reach = d;
+  bool used[3] = {size[0] == 1, size[1] == 1, size[2] == 1};
+  for (int step = 0; step < 3; ++step) {
+    int at = -1;
+    for (int i = 0; i < 3; ++i)
+      if (!used[i] && (at < 0 || stride[i] < stride[at])) at = i;
+    if (at < 0) break;
+    used[at] = true;
+    if (stride[at] < 0 || stride[at] > (1ll << 46) || (distinct && stride[at] < reach)) return false;
+    reach += stride[at] * (size[at] - 1);
+  }
+  *extent = reach;
+  return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+int salad_rope(const salad_rope_tensor* tensors, int count, int x_type, int y_type, int B, int N, int d, int rot,
+               int interleaved, const double* inv_freq, const int32_t* axis_pairs, int axes,
+               const int32_t* positions, int64_t pos_stride_b, int grid_h, int grid_w, const int32_t* origin,
+               float scale, int inverse, salad_stream_t stream) {
+  if (!tensors || count < 1 || count > 2 || !known_type(x_type) || !known_type(y_type) || !inv_freq || !axis_pairs)
+    return SALAD_ERR_INVALID_ARG;
+  if (B < 1 || N < 1 || d < 1 || rot < 2 || rot > d || rot % 2 != 0 || axes < 1 || axes > 3 || !std::isfinite(scale))
+    return SALAD_ERR_INVALID_ARG;
+  if (d > 512 || (long long)B * N >= (1ll << 31)) return SALAD_ERR_UNSUPPORTED;
+  if (!aligned(inv_freq, 8) || (positions && !aligned(positions, 4)) || pos_stride_b < 0) return SALAD_ERR_INVALID_ARG;
+  if (!positions && (grid_h < 1 || grid_w < 1)) return SALAD_ERR_INVALID_ARG;
+  RopeArgs a{};
+  long long pairs = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (i < axes && axis_pairs[i] < 0) return SALAD_ERR_INVALID_ARG;
+    pairs += i < axes ? axis_pairs[i] : 0;
+    a.axis_end[i] = (int)pairs;
+    a.origin[i] = origin ? origin[i] : 0;
+  }
+  if (pairs != rot / 2) return SALAD_ERR_INVALID_ARG;
+  const size_t xs = type_bytes(x_type), ys = type_bytes(y_type);
+  // the wide path: whole 16-byte pieces of eight values in every row
+  a.wide = d % 16 == 0 && rot % 16 == 0;
+  size_t x_bytes[2] = {0, 0}, y_bytes[2] = {0, 0};
+  bool in_place[2] = {false, false};
+  long long heads = 0;
+  for (int i = 0; i < count; ++i) {
+    const salad_rope_tensor& t = tensors[i];
+    if (!t.x || !t.y || t.heads < 1 || !aligned(t.x, xs) || !aligned(t.y, ys)) return SALAD_ERR_INVALID_ARG;
+    const int64_t sx[3] = {t.x_stride_b, t.x_stride_n, t.x_stride_h}, sy[3] = {t.y_stride_b, t.y_stride_n, t.y_stride_h};
+    int64_t ex = 0, ey = 0;
+    if (!view_extent(B, N, t.heads, d, sx, false, &ex) || !view_extent(B, N, t.heads, d, sy, true, &ey))
+      return SALAD_ERR_INVALID_ARG;
+    x_bytes[i] = (size_t)ex * xs;
+    y_bytes[i] = (size_t)ey * ys;
+    in_place[i] = t.x == t.y && x_type == y_type && sx[0] == sy[0] && sx[1] == sy[1] && sx[2] == sy[2];
+    if (!in_place[i] && overlaps(t.x, x_bytes[i], t.y, y_bytes[i])) return SALAD_ERR_INVALID_ARG;
+    for (int k = 0; k < 3; ++k)
+      a.wide = a.wide && (sx[k] * (int64_t)xs) % 16 == 0 && (sy[k] * (int64_t)ys) % 16 == 0;
+    a.wide = a.wide && aligned(t.x, 16) && aligned(t.y, 16);
+    heads += t.heads;
+    a.t[i] = RopeTensor{t.x, t.y, t.heads, sx[0], sx[1], sx[2], sy[0], sy[1], sy[2]};
+  }
+  if (heads > 65535) return SALAD_ERR_UNSUPPORTED;
+  if (count == 2) {
+    const salad_rope_tensor &p = tensors[0], &q = tensors[1];
+    if (overlaps(p.y, y_bytes[0], q.y, y_bytes[1]) || overlaps(p.y, y_bytes[0], q.x, x_bytes[1]) ||
+        overlaps(q.y, y_bytes[1], p.x, x_bytes[0])) {
+      // two views side by side in one tensor (q and k of a fused projection),
+      // each turned in place or side by side in another tensor: the same
+      // strides, and the second starts behind the first's heads of a token and
+      // ends before its next token
+      auto side_by_side = [&](const void* u, const void* v, const int64_t* su, const int64_t* sv, size_t size) {
+        const bool swap = reinterpret_cast<uintptr_t>(u) > reinterpret_cast<uintptr_t>(v);
+        const int64_t gap = (reinterpret_cast<uintptr_t>(swap ? u : v) - reinterpret_cast<uintptr_t>(swap ? v : u)) / size;
+        const int h0 = swap ? q.heads : p.heads, h1 = swap ? p.heads : q.heads;
+        return su[0] == sv[0] && su[1] == sv[1] && su[2] == sv[2] && su[2] >= d &&
+               gap >= su[2] * (h0 - 1) + d && (N == 1 || su[1] >= gap + su[2] * (h1 - 1) + d) &&
+               (B == 1 || su[0] >= (N == 1 ? gap + su[2] * (h1 - 1) + d : su[1] * N));
+      };
+      const int64_t sp[3] = {p.y_stride_b, p.y_stride_n, p.y_stride_h}, sq[3] = {q.y_stride_b, q.y_stride_n, q.y_stride_h};
+      const bool apart = !overlaps(p.y, y_bytes[0], q.x, x_bytes[1]) && !overlaps(q.y, y_bytes[1], p.x, x_bytes[0]);
+      if (!(apart || (in_place[0] && in_place[1])) || !side_by_side(p.y, q.y, sp, sq, ys)) return SALAD_ERR_INVALID_ARG;
+    }
+  }
+  a.B = B;
+  a.N = N;
+  a.d = d;
+  a.rot = rot;
+  a.interleaved = interleaved ? 1 : 0;
+  a.inverse = inverse ? 1 : 0;
+  a.axes = axes;
+  a.inv_freq = inv_freq;
+  a.positions = positions;
+  a.pos_stride_b = pos_stride_b;
+  a.grid_h = grid_h;
+  a.grid_w = grid_w;
+  a.scale = scale;
+  return launch_rope(a, x_type, y_type, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SALAD_OK
+                                                                                              : SALAD_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+int ckpt_impl(const salad_ckpt_tensor* tensors, int count, int rows, int cols, int type, int format, bool pack,
+              salad_stream_t stream) {
+  if (!tensors || count < 1 || count > kCkptMaxParts || rows < 1 || cols < 1 || !known_type(type) ||
+      (format != SALAD_INT8 && format != SALAD_E4M3))
+    return SALAD_ERR_INVALID_ARG;
+  const size_t es = type_bytes(type);
+  const int64_t groups = ((int64_t)cols + 31) / 32;
+  if (rows * groups >= (1ll << 31)) return SALAD_ERR_UNSUPPORTED;
+  CkptArgs a{};
+  a.wide = cols % 32 == 0 && rows * groups < (1ll << 30);  // (32-bit indices of 16-value pieces)
+  a.one_row = true;
+  struct Range {
+    const void* p;
+    size_t n;
+    bool out;
+  } range[3 * kCkptMaxParts];
+  for (int i = 0; i < count; ++i) {
+    const salad_ckpt_tensor& t = tensors[i];
+    if (!t.x || !t.codes || !t.scales || !aligned(t.x, es)) return SALAD_ERR_INVALID_ARG;
+    if (rows > 1 && (t.stride < cols || t.stride > (1ll << 46) / rows)) return SALAD_ERR_INVALID_ARG;
+    const int64_t stride = rows > 1 ? t.stride : cols;
+    a.wide = a.wide && aligned(t.x, 16) && aligned(t.codes, 16) && (stride * (int64_t)es) % 16 == 0;
+    a.one_row = a.one_row && stride == cols;
+    a.part[i] = CkptPart{t.x, t.x, stride, t.codes, t.scales};
+    range[3 * i] = {t.x, (size_t)(stride * (rows - 1) + cols) * es, !pack};
+    range[3 * i + 1] = {t.codes, (size_t)rows * cols, pack};
+    range[3 * i + 2] = {t.scales, (size_t)(rows * groups), pack};
+  }
+  for (int i = 0; i < 3 * count; ++i)
+    for (int j = 0; j < i; ++j) {
+      // (rows of several unpacked tensors may lie side by side in one: their
+      // ranges overlap, their elements do not when each starts inside a row)
+      const bool rows_of_one = !pack && i % 3 == 0 && j % 3 == 0 && a.part[i / 3].stride == a.part[j / 3].stride;
+      if (rows_of_one) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(range[i].p), y = reinterpret_cast<uintptr_t>(range[j].p);
+        const int64_t gap = (int64_t)((x > y ? x - y : y - x) / es);
+        if (gap >= cols && gap + cols <= a.part[i / 3].stride) continue;
+      }
+      if ((range[i].out || range[j].out) && overlaps(range[i].p, range[i].n, range[j].p, range[j].n))
+        return SALAD_ERR_INVALID_ARG;
+    }
+  a.parts = count;
+  a.rows = rows;
+  a.cols = cols;
+  return launch_ckpt(a, pack, type, format == SALAD_E4M3, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SALAD_OK
+             : SALAD_ERR_CUDA;
+}
+
+// Workspace of the backward from a checkpoint: the layer backward's (which
+// begins with the forward's), then the decoded q, k, v, the recomputed out and
+// lse, and the fp32 gradients.
+struct CkptBwdLayout {
+  size_t layer, off_qkv, off_out, off_lse, off_grads, total, tensor;
+};
+CkptBwdLayout ckpt_bwd_layout(int B, int N, int heads, int d) {
+  CkptBwdLayout L{};
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  L.layer = up(layer_bwd_layout(B, N, heads, d).total);
+  L.tensor = (size_t)B * N * heads * d;
+  size_t o = L.layer;
+  L.off_qkv = o;    o += 3 * up(L.tensor * 2);
+  L.off_out = o;    o += up(L.tensor * 2);
+  L.off_lse = o;    o += up((size_t)B * heads * N * 4);
+  L.off_grads = o;  o += up(3 * L.tensor * 4);
+  L.total = o;
+  return L;
+}
+
+}  // namespace
+
+extern "C" {
+
+int salad_ckpt_pack(const salad_ckpt_tensor* tensors, int count, int rows, int cols, int type, int format,
+                    salad_stream_t stream) {
+  return ckpt_impl(tensors, count, rows, cols, type, format, true, stream);
+}
+
+int salad_ckpt_unpack(const salad_ckpt_tensor* tensors, int count, int rows, int cols, int type, int format,
+                      salad_stream_t stream) {
+  return ckpt_impl(tensors, count, rows, cols, type, format, false, stream);
+}
+
+size_t salad_ckpt_backward_workspace_bytes(int B, int N, int num_heads, int d) {
+  if (B < 1 || N < 1 || num_heads < 1 || (d != 64 && d != 128)) return 0;
+  return ckpt_bwd_layout(B, N, num_heads, d).total;
+}
+
+int salad_attn_backward_ckpt(const uint8_t* q_codes, const uint8_t* q_scales, const uint8_t* k_codes,
+                             const uint8_t* k_scales, const uint8_t* v_codes, const uint8_t* v_scales, int format,
+                             const void* dout, int B, int N, int num_heads, int d, int block, const int32_t* row_ptr,
+                             const int32_t* col_idx, const int32_t* t_row_ptr, const int32_t* t_col_idx,
+                             int mask_per_bh, const void* w_proj, const float* gate, float softmax_scale, float eps,
+                             void* dq, void* dk, void* dv, float* dw, float* dgate, void* workspace,
+                             size_t workspace_bytes, salad_stream_t stream) {
+  const uint8_t* codes[3] = {q_codes, k_codes, v_codes};
+  const uint8_t* scales[3] = {q_scales, k_scales, v_scales};
+  for (int i = 0; i < 3; ++i)
+    if (!codes[i] || !scales[i] || !aligned(codes[i], 16)) return SALAD_ERR_INVALID_ARG;
+  if ((format != SALAD_INT8 && format != SALAD_E4M3) || !dq || !dk || !dv || !workspace || !aligned(workspace, 256))
+    return SALAD_ERR_INVALID_ARG;
+  if (!dout || !row_ptr || !col_idx || !t_row_ptr || !t_col_idx || !w_proj || !gate || !dw || !dgate)
+    return SALAD_ERR_INVALID_ARG;
+  if (!aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(dout, 16) || !aligned(w_proj, 16) ||
+      !aligned(dw, 4) || !aligned(dgate, 4) || !aligned(gate, 4) || !aligned(row_ptr, 4) || !aligned(col_idx, 4) ||
+      !aligned(t_row_ptr, 4) || !aligned(t_col_idx, 4))
+    return SALAD_ERR_INVALID_ARG;
+  if (B < 1 || N < 1 || num_heads < 1) return SALAD_ERR_INVALID_ARG;
+  if (!std::isfinite(softmax_scale) || !std::isfinite(eps) || eps < 0.f) return SALAD_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || block != 128) return SALAD_ERR_UNSUPPORTED;
+  // (all of the launches' limits, so that nothing runs before a refusal)
+  if ((long long)B * num_heads > 65534 || (long long)B * num_heads * ((N + 127) / 128) >= (1ll << 31) ||
+      (long long)B * N * num_heads >= (1ll << 31) / (d / 16))
+    return SALAD_ERR_UNSUPPORTED;
+  const CkptBwdLayout L = ckpt_bwd_layout(B, N, num_heads, d);
+  if (workspace_bytes < L.total) return SALAD_ERR_WORKSPACE;
+  const void* inputs[3] = {dq, dk, dv};
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < 3; ++j)
+      if (overlaps(inputs[i], L.tensor * 2, codes[j], L.tensor) ||
+          overlaps(inputs[i], L.tensor * 2, scales[j], L.tensor / 32) ||
+          (i < j && overlaps(inputs[i], L.tensor * 2, inputs[j], L.tensor * 2)))
+        return SALAD_ERR_INVALID_ARG;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const size_t step = (L.off_out - L.off_qkv) / 3;
+  CkptArgs ca{};
+  for (int i = 0; i < 3; ++i)
+    ca.part[i] = CkptPart{nullptr, ws + L.off_qkv + i * step, (int64_t)num_heads * d, const_cast<uint8_t*>(codes[i]),
+                          const_cast<uint8_t*>(scales[i])};
+  ca.parts = 3;
+  ca.rows = B * N;
+  ca.cols = num_heads * d;
+  ca.wide = ca.one_row = true;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (launch_ckpt(ca, false, SALAD_BF16, format == SALAD_E4M3, s) != cudaSuccess) return SALAD_ERR_CUDA;
+  const void *q = ws + L.off_qkv, *k = ws + L.off_qkv + step, *v = ws + L.off_qkv + 2 * step;
+  void* out = ws + L.off_out;
+  float* lse = reinterpret_cast<float*>(ws + L.off_lse);
+  int st = attn_forward_impl(q, k, v, B, N, num_heads, d, block, row_ptr, col_idx, w_proj, gate, softmax_scale, eps,
+                             out, workspace, L.layer, stream, mask_per_bh ? 1 : 0, nullptr, lse);
+  if (st != SALAD_OK) return st;
+  float* g = reinterpret_cast<float*>(ws + L.off_grads);
+  st = salad_attn_backward(q, k, v, out, dout, lse, B, N, num_heads, d, block, row_ptr, col_idx, t_row_ptr, t_col_idx,
+                           mask_per_bh, w_proj, gate, softmax_scale, eps, g, g + L.tensor, g + 2 * L.tensor, dw, dgate,
+                           workspace, L.layer, stream);
+  if (st != SALAD_OK) return st;
+  return launch_narrow3(g, static_cast<uint16_t*>(dq), static_cast<uint16_t*>(dk), static_cast<uint16_t*>(dv),
+                        (int64_t)L.tensor, s) == cudaSuccess
+             ? SALAD_OK
+             : SALAD_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Workspace of differential attention: the status word, then the backward's row
+// vectors and its shares of dlam.
+struct DiffLayout {
+  size_t off_rows, off_dlam, total;
+  int nb, npad;
+};
+DiffLayout diff_layout(int B, int N, int heads) {
+  DiffLayout L{};
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  L.nb = (int)(((long long)N + 127) / 128);
+  L.npad = L.nb * 128;
+  L.off_rows = 256;
+  L.off_dlam = L.off_rows + up((size_t)4 * B * heads * L.npad * 4);
+  L.total = L.off_dlam + up((size_t)B * heads * L.nb * 4);
+  return L;
+}
+
+// Checks that both passes share; fills the common arguments.
+int diff_common(DiffArgs& a, int B, int N, int heads, int d, int block, const int32_t* row_ptr, const int32_t* col_idx,
+                int mask_per_bh, const void* lam, int lam_type, float softmax_scale, void* workspace,
+                size_t workspace_bytes) {
+  if (!row_ptr || !col_idx || !lam || !workspace || B < 1 || N < 1 || heads < 1) return SALAD_ERR_INVALID_ARG;
+  if (lam_type != SALAD_F32 && lam_type != SALAD_BF16) return SALAD_ERR_INVALID_ARG;
+  if (!aligned(row_ptr, 4) || !aligned(col_idx, 4) || !aligned(lam, type_bytes(lam_type)) || !aligned(workspace, 256) ||
+      !std::isfinite(softmax_scale))
+    return SALAD_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || block != 128) return SALAD_ERR_UNSUPPORTED;
+  if (N > (1 << 30) || heads > 65535 || (long long)B * heads * ((N + 127) / 128) >= (1ll << 31) / 128)
+    return SALAD_ERR_UNSUPPORTED;
+  const DiffLayout L = diff_layout(B, N, heads);
+  if (workspace_bytes < L.total) return SALAD_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.row_ptr = row_ptr;
+  a.col_idx = col_idx;
+  a.mask_per_bh = mask_per_bh ? 1 : 0;
+  a.lam = lam;
+  a.lam_bf16 = lam_type == SALAD_BF16;
+  a.B = B;
+  a.N = N;
+  a.heads = heads;
+  a.d = d;
+  a.nb = L.nb;
+  a.npad = L.npad;
+  a.rows = reinterpret_cast<float*>(ws + L.off_rows);
+  a.dlam_part = reinterpret_cast<float*>(ws + L.off_dlam);
+  a.scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)(d / 2));
+  a.scale_log2 = a.scale * 1.4426950408889634f;
+  a.status = reinterpret_cast<uint32_t*>(ws);
+  a.wait_limit_ns = g_wait_limit_ns.load();
+  return SALAD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t salad_diff_workspace_bytes(int B, int N, int num_heads, int d) {
+  if (B < 1 || N < 1 || num_heads < 1 || (d != 64 && d != 128)) return 0;
+  return diff_layout(B, N, num_heads).total;
+}
+
+int salad_diff_forward(const void* q, const void* k, const void* v, int B, int N, int num_heads, int d, int block,
+                       const int32_t* row_ptr, const int32_t* col_idx, int mask_per_bh, const void* lam, int lam_type,
+                       float softmax_scale, void* out, void* out2, float* lse, void* workspace,
+                       size_t workspace_bytes, salad_stream_t stream) {
+  if (!q || !k || !v || !out || (out2 == nullptr) != (lse == nullptr)) return SALAD_ERR_INVALID_ARG;
+  const void* p16[] = {q, k, v, out, out2};
+  for (const void* ptr : p16)
+    if (!aligned(ptr, 16)) return SALAD_ERR_INVALID_ARG;
+  if (!aligned(lse, 4)) return SALAD_ERR_INVALID_ARG;
+  DiffArgs a{};
+  const int st = diff_common(a, B, N, num_heads, d, block, row_ptr, col_idx, mask_per_bh, lam, lam_type, softmax_scale,
+                             workspace, workspace_bytes);
+  if (st != SALAD_OK) return st;
+  const size_t bytes = (size_t)B * N * num_heads * d * 2, lse_bytes = (size_t)2 * B * num_heads * N * 4;
+  const struct {
+    const void* p;
+    size_t n;
+  } made[3] = {{out, bytes}, {out2, bytes}, {lse, lse_bytes}};
+  for (int i = 0; i < (lse ? 3 : 1); ++i) {
+    if (overlaps(made[i].p, made[i].n, q, bytes) || overlaps(made[i].p, made[i].n, k, bytes) ||
+        overlaps(made[i].p, made[i].n, v, bytes))
+      return SALAD_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(made[i].p, made[i].n, made[j].p, made[j].n)) return SALAD_ERR_INVALID_ARG;
+  }
+  CUtensorMap tq, tk, tv, to, to2;
+  if (!make_bnhd_map(&tq, q, B, N, num_heads, d, 128) || !make_bnhd_map(&tk, k, B, N, num_heads, d, 128) ||
+      !make_bnhd_map(&tv, v, B, N, num_heads, d, 128) || !make_bnhd_map(&to, out, B, N, num_heads, d, 128) ||
+      !make_bnhd_map(&to2, out2 ? out2 : out, B, N, num_heads, d, 128))
+    return SALAD_ERR_CUDA;
+  a.tm_q = &tq;
+  a.tm_k = &tk;
+  a.tm_v = &tv;
+  a.tm_out = &to;
+  a.tm_out2 = &to2;
+  a.lse = lse;
+  return launch_diff_forward(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SALAD_OK : SALAD_ERR_CUDA;
+}
+
+int salad_diff_backward(const void* q, const void* k, const void* v, const void* out, const void* out2,
+                        const void* dout, const float* lse, int B, int N, int num_heads, int d, int block,
+                        const int32_t* row_ptr, const int32_t* col_idx, const int32_t* t_row_ptr,
+                        const int32_t* t_col_idx, int mask_per_bh, const void* lam, int lam_type,
+                        float softmax_scale, void* dq, void* dk, void* dv, void* dlam, void* workspace,
+                        size_t workspace_bytes, salad_stream_t stream) {
+  if (!q || !k || !v || !out || !out2 || !dout || !lse || !t_row_ptr || !t_col_idx || !dq || !dk || !dv || !dlam)
+    return SALAD_ERR_INVALID_ARG;
+  const void* p16[] = {q, k, v, out, out2, dout, dq, dk, dv};
+  for (const void* ptr : p16)
+    if (!aligned(ptr, 16)) return SALAD_ERR_INVALID_ARG;
+  if (!aligned(lse, 4) || !aligned(t_row_ptr, 4) || !aligned(t_col_idx, 4)) return SALAD_ERR_INVALID_ARG;
+  DiffArgs a{};
+  const int st = diff_common(a, B, N, num_heads, d, block, row_ptr, col_idx, mask_per_bh, lam, lam_type, softmax_scale,
+                             workspace, workspace_bytes);
+  if (st != SALAD_OK) return st;
+  if (!aligned(dlam, type_bytes(lam_type))) return SALAD_ERR_INVALID_ARG;
+  const size_t bytes = (size_t)B * N * num_heads * d * 2;
+  const void* made[3] = {dq, dk, dv};
+  const void* read[6] = {q, k, v, out, out2, dout};
+  for (int i = 0; i < 3; ++i) {
+    for (const void* x : read)
+      if (overlaps(made[i], bytes, x, bytes)) return SALAD_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlaps(made[i], bytes, made[j], bytes)) return SALAD_ERR_INVALID_ARG;
+  }
+  CUtensorMap tq, tk, tv, tdo;
+  if (!make_bnhd_map(&tq, q, B, N, num_heads, d, 128) || !make_bnhd_map(&tk, k, B, N, num_heads, d, 128) ||
+      !make_bnhd_map(&tv, v, B, N, num_heads, d, 128) || !make_bnhd_map(&tdo, dout, B, N, num_heads, d, 128))
+    return SALAD_ERR_CUDA;
+  a.tm_q = &tq;
+  a.tm_k = &tk;
+  a.tm_v = &tv;
+  a.tm_do = &tdo;
+  a.t_row_ptr = t_row_ptr;
+  a.t_col_idx = t_col_idx;
+  a.out = static_cast<const uint16_t*>(out);
+  a.out2 = static_cast<const uint16_t*>(out2);
+  a.dout = static_cast<const uint16_t*>(dout);
+  a.lse = const_cast<float*>(lse);
+  a.dq = static_cast<uint16_t*>(dq);
+  a.dk = static_cast<uint16_t*>(dk);
+  a.dv = static_cast<uint16_t*>(dv);
+  a.dlam = dlam;
+  return launch_diff_backward(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SALAD_OK : SALAD_ERR_CUDA;
+}
+
+int salad_diff_decode(const void* q, const void* k, const void* v, int B, int Nq, int capacity, int num_heads, int d,
+                      const int32_t* lens, const void* lam, int lam_type, float softmax_scale, void* out,
+                      salad_stream_t stream) {
+  if (!q || !k || !v || !lens || !lam || !out || B < 1 || Nq < 1 || capacity < 1 || num_heads < 1)
+    return SALAD_ERR_INVALID_ARG;
+  if (lam_type != SALAD_F32 && lam_type != SALAD_BF16) return SALAD_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(lens, 4) ||
+      !aligned(lam, type_bytes(lam_type)) || !std::isfinite(softmax_scale))
+    return SALAD_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return SALAD_ERR_UNSUPPORTED;
+  if ((long long)B * num_heads >= (1ll << 31) / 16 || Nq > 262140 || capacity > (1 << 30)) return SALAD_ERR_UNSUPPORTED;
+  const size_t row = (size_t)num_heads * d * 2, qb = (size_t)B * Nq * row, kb = (size_t)B * capacity * row;
+  if (overlaps(out, qb, q, qb) || overlaps(out, qb, k, kb) || overlaps(out, qb, v, kb)) return SALAD_ERR_INVALID_ARG;
+  DiffDecodeArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.lens = lens;
+  a.lam = lam;
+  a.out = static_cast<uint16_t*>(out);
+  a.lam_bf16 = lam_type == SALAD_BF16;
+  a.B = B;
+  a.Nq = Nq;
+  a.cap = capacity;
+  a.heads = num_heads;
+  a.d = d;
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)(d / 2));
+  a.scale_log2 = scale * 1.4426950408889634f;
+  return launch_diff_decode(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SALAD_OK : SALAD_ERR_CUDA;
+}
+
 int salad_check_status(void* workspace, salad_stream_t stream) {
   if (!workspace) return SALAD_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -1,0 +1,387 @@
+// Differential attention over the kept key blocks: each head's q and k (d wide)
+// hold two halves of h = d/2 features, each half has its own softmax map over
+// the same keys, and the maps' difference weighs the values:
+//   P_m = softmax(scale Q_m K_m^T) over the kept keys (m = 1, 2)
+//   out = P_1 V - lam[head] P_2 V          (0 for a query whose blocks keep no key)
+// One CTA takes one 128-row query tile of one (b, h) and walks its kept key
+// tiles; both maps read the same K and V tiles.
+//
+// Tensor memory (512 columns): S_1 [0,128), S_2 [128,256), O_1 [256,256+d),
+// O_2 [384,384+d); P_m as bf16 over the first 64 columns of S_m, so S_m of the
+// next tile follows P_m V in the issue order.  The maps alternate: while the four
+// softmax warps of map 1 work, the tensor cores run P_2 V and S_2 of the next
+// tile, and the other way round.
+// Warp roles, 320 threads: warp 0 TMA producer (K and V rings of three tiles),
+// warp 1 tcgen05 issuer and owner of the tensor memory, warps 2-5 softmax of map
+// 1 and warps 6-9 of map 2, one thread a query row.  The running maximum only
+// moves (and O_m is rescaled in tensor memory) when it grows by more than 2^8.
+// The row sum adds the bf16-rounded p that the value product reads, so the
+// rounding of a dominant key cancels in O / l.  At the end the two warp groups
+// exchange the row sums and each writes half of the features of its row.
+//
+// Bound by the exponentials: 2 x 128 x 128 a tile pair, 16 a clock and SM on the
+// special-function unit, against 1,536 clocks of products at d = 128; one pair in
+// four therefore runs on the FMA pipe (exp2_fma_x2).  Every barrier wait is
+// bounded; on a time-out the kernel records it and drains.
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace salad {
+namespace {
+
+constexpr int kDiffThreads = 320;
+constexpr uint64_t kDiffDrainNs = 1000000000ull;
+constexpr float kDiffRescale = 8.0f;  // log2 units
+constexpr float kLn2 = 0.69314718055994531f;
+
+struct DiffShared {
+  uint64_t q_full;
+  uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
+  uint64_t s_full[2];   // per map: S of the current tile is in tensor memory (and the P V before it is done)
+  uint64_t p_full[2];   // per map: the four softmax warps have written P
+  uint64_t o_full;      // every product is done
+  uint64_t drain;
+  uint32_t tmem_base;
+  volatile int abort_flag;
+  float sum[2][128];    // per map: row sums, for the other group's features
+};
+
+template <int D>
+struct DiffCfg {
+  static constexpr int DCH = D / 64;
+  static constexpr int TILE = 128 * D * 2;
+  static constexpr int STAGES = 3;
+  static constexpr int OFF_Q = 0;                       // later the staged output
+  static constexpr int OFF_K = TILE;                    // stage 0 later holds the staged second output
+  static constexpr int OFF_V = OFF_K + STAGES * TILE;
+  static constexpr int OFF_BAR = OFF_V + STAGES * TILE;
+  static constexpr int SMEM_USED = OFF_BAR + (int)sizeof(DiffShared) + 1024;
+  // at least 120 KB so that one CTA (and its 512 TMEM columns) owns the SM
+  static constexpr int SMEM = SMEM_USED > 122880 ? SMEM_USED : 122880;
+  static constexpr uint32_t TM_S = 0, TM_O = 256;       // + 128 per map
+  static constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false);
+  static constexpr uint32_t IDESC_PV = idesc_bf16(128, D, false, true);
+  static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+__device__ __forceinline__ void diff_timeout(DiffShared* sh, uint32_t* status) {
+  sh->abort_flag = 1;
+  atomicOr(status, kStatusTimeout);
+}
+
+__device__ __forceinline__ float lambda_of(const void* lam, int bf16, int h) {
+  return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(lam)[h] << 16) : static_cast<const float*>(lam)[h];
+}
+
+// TRAIN: also O_2 / l_2 and the log-sum-exps of both maps.
+template <int D, bool TRAIN>
+__global__ void __launch_bounds__(kDiffThreads, 1)
+    diff_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_out,
+                    const __grid_constant__ CUtensorMap tm_out2, const int32_t* __restrict__ row_ptr,
+                    const int32_t* __restrict__ col_idx, const void* __restrict__ lam, int lam_bf16,
+                    float* __restrict__ lse, int N, int heads, int nb, int mask_per_bh, float scale_log2,
+                    uint32_t* status, uint64_t limit_ns) {
+  using C = DiffCfg<D>;
+  extern __shared__ uint8_t diff_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(diff_smem_raw) + 1023) & ~uintptr_t(1023));
+  DiffShared* sh = reinterpret_cast<DiffShared*>(smem + C::OFF_BAR);
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int qt = blockIdx.x % nb, bh = blockIdx.x / nb, b = bh / heads, h = bh % heads;
+  const int mrow = (mask_per_bh ? bh : h) * nb + qt;
+  const int mask_rows = (mask_per_bh ? (int)(gridDim.x / nb) : heads) * nb;
+  const int c0 = row_ptr[mrow];
+  const int n = debug_row_ok(row_ptr, col_idx, mrow, mask_rows, nb, true, status) ? row_ptr[mrow + 1] - c0 : 0;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&sh->q_full, 1);
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&sh->k_full[s], 1);
+      mbar_init(&sh->k_empty[s], 1);
+      mbar_init(&sh->v_full[s], 1);
+      mbar_init(&sh->v_empty[s], 1);
+    }
+    for (int m = 0; m < 2; ++m) {
+      mbar_init(&sh->s_full[m], 1);
+      mbar_init(&sh->p_full[m], 4);
+    }
+    mbar_init(&sh->o_full, 1);
+    mbar_init(&sh->drain, 1);
+    sh->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&sh->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_map(&tm_k);
+      tma_prefetch_map(&tm_v);
+      bool ok = true;
+      int kl = 0, vl = 0;
+      mbar_arrive_expect_tx(&sh->q_full, C::TILE);
+#pragma unroll
+      for (int ch = 0; ch < C::DCH; ++ch)
+        tma_load_3d(smem + C::OFF_Q + ch * 16384, &tm_q, &sh->q_full, h * D + ch * 64, qt * 128, b);
+      for (int j = 0; j < n; ++j) {
+        const int s = j % C::STAGES, col = col_idx[c0 + j];
+        const uint32_t ph = (uint32_t)((j / C::STAGES) & 1);
+        if (sh->abort_flag || !mbar_wait(&sh->k_empty[s], ph ^ 1, limit_ns)) { ok = false; break; }
+        mbar_arrive_expect_tx(&sh->k_full[s], C::TILE);
+#pragma unroll
+        for (int ch = 0; ch < C::DCH; ++ch)
+          tma_load_3d(smem + C::OFF_K + s * C::TILE + ch * 16384, &tm_k, &sh->k_full[s], h * D + ch * 64, col * 128, b);
+        ++kl;
+        if (sh->abort_flag || !mbar_wait(&sh->v_empty[s], ph ^ 1, limit_ns)) { ok = false; break; }
+        mbar_arrive_expect_tx(&sh->v_full[s], C::TILE);
+#pragma unroll
+        for (int ch = 0; ch < C::DCH; ++ch)
+          tma_load_3d(smem + C::OFF_V + s * C::TILE + ch * 16384, &tm_v, &sh->v_full[s], h * D + ch * 64, col * 128, b);
+        ++vl;
+      }
+      if (!ok) diff_timeout(sh, status);
+      // every copy this thread started lands before the CTA exits
+      mbar_wait(&sh->q_full, 0, kDiffDrainNs);
+      for (int i = (kl > C::STAGES ? kl - C::STAGES : 0); i < kl; ++i)
+        mbar_wait(&sh->k_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), kDiffDrainNs);
+      for (int i = (vl > C::STAGES ? vl - C::STAGES : 0); i < vl; ++i)
+        mbar_wait(&sh->v_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), kDiffDrainNs);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && n > 0) {
+      bool ok = mbar_wait(&sh->q_full, 0, limit_ns);
+      const uint32_t q_s = sbase + C::OFF_Q;
+      // S_m of tile j: the k-steps of the map's half of the features
+      auto issue_s = [&](int m, int j) {
+        const uint32_t kt = sbase + C::OFF_K + (j % C::STAGES) * C::TILE;
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk) {
+          const int f = m * (D / 32) + kk;
+          const uint32_t off = (f / 4) * 16384 + (f % 4) * 32;
+          mma_bf16_ss(tmem + C::TM_S + 128 * m, sw128_desc(q_s + off, 16, 1024), sw128_desc(kt + off, 16, 1024),
+                      C::IDESC_S, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&sh->s_full[m]);
+      };
+      auto issue_pv = [&](int m, int j) {
+        const uint32_t vt = sbase + C::OFF_V + (j % C::STAGES) * C::TILE;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_bf16_ts(tmem + C::TM_O + 128 * m, tmem + C::TM_S + 128 * m + kk * 8,
+                      sw128_desc(vt + kk * 2048, 16384, 1024), C::IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
+      };
+      auto wait_k = [&](int j) {
+        return mbar_wait(&sh->k_full[j % C::STAGES], (uint32_t)((j / C::STAGES) & 1), limit_ns);
+      };
+      ok = ok && wait_k(0);
+      if (ok) {
+        tc_fence_after();
+        issue_s(0, 0);
+        issue_s(1, 0);
+        mma_commit(&sh->k_empty[0]);
+      }
+      for (int j = 0; ok && j < n; ++j) {
+        const int s = j % C::STAGES;
+        if (!mbar_wait(&sh->v_full[s], (uint32_t)((j / C::STAGES) & 1), limit_ns) || (j + 1 < n && !wait_k(j + 1))) {
+          ok = false;
+          break;
+        }
+        for (int m = 0; m < 2; ++m) {
+          if (sh->abort_flag || !mbar_wait(&sh->p_full[m], (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
+          tc_fence_after();
+          issue_pv(m, j);
+          if (m == 1) mma_commit(&sh->v_empty[s]);
+          if (j + 1 < n) {
+            issue_s(m, j + 1);
+            if (m == 1) mma_commit(&sh->k_empty[(j + 1) % C::STAGES]);
+          }
+        }
+      }
+      if (ok)
+        mma_commit(&sh->o_full);
+      else
+        diff_timeout(sh, status);
+      // every product has ended before the tensor memory is given back, also when a softmax warp gave up
+      mma_commit(&sh->drain);
+      mbar_wait(&sh->drain, 0, kDiffDrainNs);
+    }
+  } else {
+    const int m = (warp - 2) >> 2;  // the map
+    const int quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t s_addr = lane_addr + C::TM_S + 128 * m, o_addr = lane_addr + C::TM_O + 128 * m;
+    const uint64_t c2 = f32x2_pack(scale_log2, scale_log2);
+    float m_ref = -INFINITY, l = 0.f, le = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      const int valid = N - col_idx[c0 + j] * 128;  // real keys of the tile
+      if (!mbar_wait_warp(&sh->s_full[m], (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t sr[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
+      tmem_ld_wait();
+      if (valid < 128) {
+#pragma unroll
+        for (int i = 0; i < 128; ++i)
+          if (i >= valid) sr[i] = __float_as_uint(-INFINITY);
+      }
+      float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 128; i += 8) {
+        m0 = fmax3(m0, __uint_as_float(sr[i + 0]), __uint_as_float(sr[i + 1]));
+        m1 = fmax3(m1, __uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3]));
+        m2 = fmax3(m2, __uint_as_float(sr[i + 4]), __uint_as_float(sr[i + 5]));
+        m3 = fmax3(m3, __uint_as_float(sr[i + 6]), __uint_as_float(sr[i + 7]));
+      }
+      const float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+      float alpha = 1.f;
+      bool rescale = false;
+      if (m_ref == -INFINITY) {
+        m_ref = mt;
+      } else if ((mt - m_ref) * scale_log2 > kDiffRescale) {
+        alpha = ex2_approx((m_ref - mt) * scale_log2);
+        m_ref = mt;
+        rescale = true;
+      }
+      if (__any_sync(0xffffffffu, rescale)) {
+        // (the product that wrote O last came before S of this tile)
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t rr[32];
+          tmem_ld32(o_addr + 32 * c, rr);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) rr[i] = __float_as_uint(__uint_as_float(rr[i]) * alpha);
+          tmem_st32(o_addr + 32 * c, rr);
+        }
+      }
+      const uint64_t nmb2 = f32x2_pack(-m_ref * scale_log2, -m_ref * scale_log2);
+      uint64_t acc0 = 0, acc1 = 0, acce = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int e = 32 * c + 2 * i;
+          const uint64_t x = f32x2_fma(f32x2_pack(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2, nmb2);
+          float p0, p1;
+          if ((i & 3) == 3) {
+            exp2_fma_x2(x, p0, p1);
+          } else {
+            float x0, x1;
+            f32x2_unpack(x, x0, x1);
+            p0 = ex2_approx(x0);
+            p1 = ex2_approx(x1);
+          }
+          pk[i] = pack_bf16x2(p0, p1);
+          if (TRAIN) acce = f32x2_add(acce, f32x2_pack(p0, p1));
+          const uint64_t pp = f32x2_pack(bf16_lo_to_f32(pk[i]), bf16_hi_to_f32(pk[i]));
+          if (i & 1)
+            acc1 = f32x2_add(acc1, pp);
+          else
+            acc0 = f32x2_add(acc0, pp);
+        }
+        tmem_st16(s_addr + 16 * c, pk);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->p_full[m]);
+      float a0, a1;
+      f32x2_unpack(f32x2_add(acc0, acc1), a0, a1);
+      l = l * alpha + (a0 + a1);
+      if (TRAIN) {
+        f32x2_unpack(acce, a0, a1);
+        le = le * alpha + (a0 + a1);
+      }
+    }
+    if (ok && n > 0) ok = mbar_wait_warp(&sh->o_full, 0, limit_ns);
+    if (!ok) diff_timeout(sh, status);
+    const int row = qt * 128 + r;
+    if (TRAIN && ok && row < N) {
+      const size_t BH = gridDim.x / nb;
+      lse[((size_t)m * BH + bh) * N + row] = n > 0 ? (m_ref * scale_log2 + log2f(le)) * kLn2 : -INFINITY;
+    }
+    sh->sum[m][r] = l;
+    named_bar_sync(1, 256);  // (reached by every softmax thread, after a time-out too)
+    tc_fence_after();
+    // features [m D/2, m D/2 + D/2) of this row: out = O_1 / l_1 - lam O_2 / l_2
+    const float lh = lambda_of(lam, lam_bf16, h);
+    const float i1 = n > 0 ? 1.f / sh->sum[0][r] : 0.f, i2 = n > 0 ? 1.f / sh->sum[1][r] : 0.f;
+    if (n == 0) mbar_wait_warp(&sh->q_full, 0, limit_ns);  // the Q buffer is written over: its load must have landed
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      const int f0 = m * (D / 2) + 32 * c;  // 32 features
+      uint32_t a[32], o2[32], pk[16], pk2[16];
+      if (ok && n > 0) {
+        tmem_ld32(lane_addr + C::TM_O + f0, a);
+        tmem_ld32(lane_addr + C::TM_O + 128 + f0, o2);
+        tmem_ld_wait();
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float x0 = 0.f, x1 = 0.f, y0 = 0.f, y1 = 0.f;
+        if (n > 0) {
+          y0 = __uint_as_float(o2[2 * i]) * i2;
+          y1 = __uint_as_float(o2[2 * i + 1]) * i2;
+          x0 = fmaf(__uint_as_float(a[2 * i]), i1, -lh * y0);
+          x1 = fmaf(__uint_as_float(a[2 * i + 1]), i1, -lh * y1);
+        }
+        pk[i] = pack_bf16x2(x0, x1);
+        pk2[i] = pack_bf16x2(y0, y1);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t piece = (uint32_t)(f0 / 8 + t), at = (piece / 8) * 16384 + sw128_offset((uint32_t)r, piece % 8);
+        st_shared_v4(sbase + C::OFF_Q + at, pk[4 * t], pk[4 * t + 1], pk[4 * t + 2], pk[4 * t + 3]);
+        if (TRAIN) st_shared_v4(sbase + C::OFF_K + at, pk2[4 * t], pk2[4 * t + 1], pk2[4 * t + 2], pk2[4 * t + 3]);
+      }
+    }
+    fence_proxy_async_smem();
+    named_bar_sync(1, 256);
+    if (warp == 2 && lane == 0 && !sh->abort_flag) {
+#pragma unroll
+      for (int ch = 0; ch < C::DCH; ++ch) {
+        tma_store_3d(&tm_out, smem + C::OFF_Q + ch * 16384, h * D + ch * 64, qt * 128, b);
+        if (TRAIN) tma_store_3d(&tm_out2, smem + C::OFF_K + ch * 16384, h * D + ch * 64, qt * 128, b);
+      }
+      bulk_commit_group();
+      bulk_wait_group_read0();
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, bool TRAIN>
+cudaError_t launch_diff_fwd_t(const DiffArgs& a, cudaStream_t s) {
+  using C = DiffCfg<D>;
+  cudaError_t e = cudaFuncSetAttribute(diff_fwd_kernel<D, TRAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  diff_fwd_kernel<D, TRAIN><<<a.B * a.heads * a.nb, kDiffThreads, C::SMEM, s>>>(
+      *a.tm_q, *a.tm_k, *a.tm_v, *a.tm_out, *a.tm_out2, a.row_ptr, a.col_idx, a.lam, a.lam_bf16, a.lse, a.N, a.heads,
+      a.nb, a.mask_per_bh, a.scale_log2, a.status, a.wait_limit_ns);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_diff_forward(const DiffArgs& a, cudaStream_t s) {
+  if (a.lse != nullptr) return a.d == 64 ? launch_diff_fwd_t<64, true>(a, s) : launch_diff_fwd_t<128, true>(a, s);
+  return a.d == 64 ? launch_diff_fwd_t<64, false>(a, s) : launch_diff_fwd_t<128, false>(a, s);
+}
+
+}  // namespace salad

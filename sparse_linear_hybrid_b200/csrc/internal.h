@@ -185,6 +185,77 @@ size_t topk_workspace_bytes(int B, int N, int heads, int d, int block);
 cudaError_t launch_topk_mask(const TopkArgs& a, cudaStream_t s);
 constexpr int kTopkMaxBlocks = 2048;  // the selection keeps one row of scores per query block in shared memory
 
+// Rotary positions (rope.cu).
+struct RopeTensor {
+  const void* x;
+  void* y;
+  int heads;                // 0: no second tensor
+  int64_t xb, xn, xh;       // element strides of a sequence, a token, a head
+  int64_t yb, yn, yh;
+};
+struct RopeArgs {
+  RopeTensor t[2];          // q and k
+  int B, N, d, rot, interleaved, inverse, axes;
+  int axis_end[3];          // pairs [0, axis_end[0]) follow axis 0, and so on
+  const double* inv_freq;   // [rot/2]
+  const int32_t* positions; // [B or 1][N][axes], or null: a T x H x W grid (or a plain count) from origin
+  int64_t pos_stride_b;
+  int grid_h, grid_w, origin[3];
+  float scale;
+  bool wide;                // widths and alignment allow 16-byte pieces
+  int heads_per_warp;       // set by the launch
+};
+cudaError_t launch_rope(const RopeArgs& a, int x_type, int y_type, cudaStream_t s);
+
+// Activation checkpoints in 8 bits (ckpt.cu).
+struct CkptPart {
+  const void* x;    // pack: the values
+  void* y;          // unpack: the values
+  int64_t stride;   // elements from row to row of x or y
+  uint8_t* codes;   // [rows][cols]
+  uint8_t* scales;  // [rows][ceil(cols/32)]
+};
+constexpr int kCkptMaxParts = 4;
+struct CkptArgs {
+  CkptPart part[kCkptMaxParts];
+  int parts, rows, cols;
+  bool wide, one_row;  // 16 values a lane; all rows lie one after another
+};
+cudaError_t launch_ckpt(const CkptArgs& a, bool pack, int type, bool fp8, cudaStream_t s);
+// [3][count] fp32 to three bf16 arrays (count a multiple of 8).
+cudaError_t launch_narrow3(const float* x, uint16_t* y0, uint16_t* y1, uint16_t* y2, int64_t count, cudaStream_t s);
+
+// Differential attention (diff.cu, diff_bwd.cu, diff_decode.cu); raster blocks of 128 tokens.
+struct DiffArgs {
+  const CUtensorMap *tm_q, *tm_k, *tm_v;  // box (64, 128, 1)
+  const CUtensorMap *tm_out, *tm_out2;    // forward (tm_out2: with lse)
+  const CUtensorMap* tm_do;               // backward
+  const int32_t *row_ptr, *col_idx, *t_row_ptr, *t_col_idx;
+  const void* lam;                        // [heads], bf16 or fp32
+  int lam_bf16;
+  float* lse;                             // fp32 [2][B*Hh][N], natural log; null: forward without gradients
+  const uint16_t *out, *out2, *dout;      // backward
+  uint16_t *dq, *dk, *dv;
+  void* dlam;
+  float* rows;                            // workspace: [4][B*Hh][npad]
+  float* dlam_part;                       // workspace: [B*Hh][nb]
+  int B, N, heads, d, nb, npad, mask_per_bh;
+  float scale, scale_log2;
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+};
+cudaError_t launch_diff_forward(const DiffArgs& a, cudaStream_t s);
+cudaError_t launch_diff_backward(const DiffArgs& a, cudaStream_t s);
+struct DiffDecodeArgs {
+  const uint16_t *q, *k, *v;  // bf16 [B][Nq][Hh][d], [B][cap][Hh][d]
+  const int32_t* lens;        // [B]
+  const void* lam;
+  uint16_t* out;
+  int lam_bf16, B, Nq, cap, heads, d;
+  float scale_log2;
+};
+cudaError_t launch_diff_decode(const DiffDecodeArgs& a, cudaStream_t s);
+
 // Status word bits written by kernels.
 constexpr uint32_t kStatusTimeout = 1u;
 constexpr uint32_t kStatusBadMask = 2u;  // debug builds: a malformed mask row was skipped
