@@ -21,6 +21,7 @@ import ctypes
 import dataclasses
 import math
 import os
+import struct
 
 import numpy as np
 import torch
@@ -45,14 +46,11 @@ _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _FORMATS = {"int8": 0, "e4m3": 1}
 
 
-class _RopeTensor(ctypes.Structure):
-    _fields_ = ([("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int)]
-                + [(f"{a}_stride_{s}", ctypes.c_int64) for a in "xy" for s in "bnh"])
-
-
-class _CkptTensor(ctypes.Structure):
-    _fields_ = [("x", ctypes.c_void_p), ("stride", ctypes.c_int64), ("codes", ctypes.c_void_p),
-                ("scales", ctypes.c_void_p)]
+# salad_rope_tensor and salad_ckpt_tensor as bytes (a fraction of what filling ctypes structures costs a small call)
+_ROPE_TENSOR = struct.Struct("PPi4x6q").pack
+_CKPT_TENSOR = struct.Struct("PqPP").pack
+_INT3 = struct.Struct("3i").pack
+_NULL = contextlib.nullcontext()
 
 
 class SaladError(RuntimeError):
@@ -172,8 +170,8 @@ def _check(status: int, what: str) -> None:
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # (the current stream's handle without a Stream object around it)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -543,16 +541,21 @@ def attn_forward_static(q, k, v, row_ptr, col_idx, w_proj, gate, block: int, sof
 
 def _on(*tensors):
     """(context that makes the tensors' device current, that device); all have to be on one CUDA device."""
+    dev = None
     for t in tensors:
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError("the tensors must be CUDA tensors (libsalad has no CPU path)")
-    dev = tensors[0].device
-    for t in tensors:
-        if t.device != dev:
-            raise ValueError(f"the tensors lie on several devices: {dev} and {t.device}")
-    if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext(), dev
-    return torch.cuda.device(dev), dev
+        d = t.get_device()
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"the tensors lie on several devices: cuda:{dev} and cuda:{d}")
+    return (_NULL if dev == torch.cuda.current_device() else torch.cuda.device(dev)), tensors[0].device
+
+
+def _new_like(x, dtype):
+    """Contiguous memory of x's shape."""
+    return torch.empty_like(x) if x.dtype == dtype and x.is_contiguous() else x.new_empty(x.shape, dtype=dtype)
 
 
 def rope_inv_freq(rot: int, base: float = 10000.0, sections=None, scaling: str | None = None, factor: float = 1.0,
@@ -592,58 +595,66 @@ def rope_inv_freq(rot: int, base: float = 10000.0, sections=None, scaling: str |
 
 def _rope(q, k, inv_freq, sections, interleaved, scale, positions, grid, origin, q_out, k_out, out_dtype, inverse,
           stream):
-    xs = [q] if k is None else [q, k]
-    ctx, _ = _on(*xs, inv_freq, *([] if positions is None else [positions]))
-    B, N, _, d = q.shape
-    ys = [q_out, k_out][:len(xs)]
+    xs = (q,) if k is None else (q, k)
     if k is None and k_out is not None:
         raise ValueError("k_out without k")
+    ctx, _ = _on(*xs, inv_freq) if positions is None else _on(*xs, inv_freq, positions)
+    if q.dim() != 4:
+        raise ValueError("q and k must be [B, N, heads, d] with the same B, N and d")
+    B, N, _, d = q.shape
+    kind = q.dtype
+    if kind not in _TYPES or (out_dtype is not None and out_dtype not in _TYPES):
+        raise TypeError("q, k and the outputs must be fp32, bf16 or fp16")
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise TypeError("inv_freq must be a contiguous fp64 vector")
+    rot = 2 * inv_freq.numel()
+    sections = [rot // 2] if sections is None else [int(n) for n in sections]
+    axes = len(sections)
+    if not 1 <= axes <= 3:
+        raise ValueError("one to three sections")
+    pos_ptr, pos_b, gh, gw = None, 0, 1, 1
+    if positions is not None:
+        if grid is not None:
+            raise ValueError("give positions or a grid, not both")
+        if positions.dtype != torch.int32:
+            raise TypeError(f"positions must be int32, got {positions.dtype}")
+        shape = tuple(positions.shape)
+        one = (N,) if axes == 1 else (N, axes)
+        if shape not in (one, (1, *one), (B, *one)) or not positions.is_contiguous():
+            raise ValueError(f"positions must be contiguous [B, N{', axes' if axes > 1 else ''}] or without B")
+        pos_ptr, pos_b = positions.data_ptr(), (N * axes if len(shape) > len(one) and shape[0] > 1 else 0)
+    elif grid is not None:
+        T, gh, gw = (int(n) for n in grid)
+        if axes != 3 or T * gh * gw != N:
+            raise ValueError(f"a grid needs three sections and {T} * {gh} * {gw} tokens, got {axes} and {N}")
+    elif axes != 1:
+        raise ValueError("several sections need positions or a grid")
+    ys, packed = [], b""
     with ctx:
-        arr = (_RopeTensor * len(xs))()
-        for i, x in enumerate(xs):
-            if x.dim() != 4 or (x.shape[0], x.shape[1], x.shape[3]) != (B, N, d):
+        for x, y in zip(xs, (q_out, k_out)):
+            if x.dim() != 4 or x.shape[0] != B or x.shape[1] != N or x.shape[3] != d:
                 raise ValueError("q and k must be [B, N, heads, d] with the same B, N and d")
-            if x.dtype not in _TYPES or x.dtype != q.dtype:
+            if x.dtype != kind:
                 raise TypeError("q and k must share one of fp32, bf16, fp16")
-            if ys[i] is None:
-                ys[i] = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-            y = ys[i]
-            if y.shape != x.shape or y.device != x.device or y.dtype not in _TYPES or y.dtype != ys[0].dtype:
-                raise ValueError("outputs must have their input's shape and device, and one type")
-            if out_dtype is not None and y.dtype != out_dtype:
-                raise TypeError(f"the output is {y.dtype}, not {out_dtype}")
-            if d > 1 and (x.stride(3) != 1 or y.stride(3) != 1):
+            if y is None:
+                y = _new_like(x, out_dtype or (ys[0].dtype if ys else kind))
+            else:
+                _on(q, y)
+                if y.shape != x.shape or y.dtype not in _TYPES or (ys and y.dtype != ys[0].dtype):
+                    raise ValueError("outputs must have their input's shape, and one type")
+                if out_dtype is not None and y.dtype != out_dtype:
+                    raise TypeError(f"the output is {y.dtype}, not {out_dtype}")
+            xb, xn, xh, xf = x.stride()
+            yb, yn, yh, yf = y.stride()
+            if d > 1 and (xf != 1 or yf != 1):
                 raise ValueError("the features of a head must be contiguous")
-            arr[i] = _RopeTensor(x.data_ptr(), y.data_ptr(), x.shape[2], *x.stride()[:3], *y.stride()[:3])
-        if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
-            raise TypeError("inv_freq must be a contiguous fp64 vector")
-        rot = 2 * inv_freq.numel()
-        sections = [rot // 2] if sections is None else [int(n) for n in sections]
-        axes = len(sections)
-        pos_ptr, pos_b, gh, gw = None, 0, 1, 1
-        if positions is not None:
-            if grid is not None:
-                raise ValueError("give positions or a grid, not both")
-            if positions.dtype != torch.int32:
-                raise TypeError(f"positions must be int32, got {positions.dtype}")
-            p = positions if axes > 1 else positions.unsqueeze(-1)
-            p = p if p.dim() == 3 else p.unsqueeze(0)
-            if p.dim() != 3 or p.shape[0] not in (1, B) or p.shape[1:] != (N, axes) or not p.is_contiguous():
-                raise ValueError(f"positions must be contiguous [B, N{', axes' if axes > 1 else ''}] or without B")
-            pos_ptr, pos_b = ctypes.c_void_p(p.data_ptr()), (N * axes if p.shape[0] > 1 else 0)
-        elif grid is not None:
-            T, gh, gw = (int(n) for n in grid)
-            if axes != 3 or T * gh * gw != N:
-                raise ValueError(f"a grid needs three sections and {T} * {gh} * {gw} tokens, got {axes} and {N}")
-        elif axes != 1:
-            raise ValueError("several sections need positions or a grid")
-        if N == 0 or B == 0:
-            return ys
-        org = (ctypes.c_int32 * 3)(*(list(origin) + [0, 0, 0])[:3])
-        _check(lib().salad_rope(arr, len(xs), _TYPES[q.dtype], _TYPES[ys[0].dtype], B, N, d, rot,
-                                int(bool(interleaved)), ctypes.c_void_p(inv_freq.data_ptr()),
-                                (ctypes.c_int32 * max(axes, 1))(*sections), axes, pos_ptr, pos_b, gh, gw, org,
-                                float(scale), inverse, _stream(stream)), "salad_rope")
+            packed += _ROPE_TENSOR(x.data_ptr(), y.data_ptr(), x.shape[2], xb, xn, xh, yb, yn, yh)
+            ys.append(y)
+        if B and N:
+            o = tuple(origin)
+            _check(lib().salad_rope(packed, len(xs), _TYPES[kind], _TYPES[ys[0].dtype], B, N, d, rot, bool(interleaved),
+                                    inv_freq.data_ptr(), _INT3(*sections, *(0,) * (3 - axes)), axes, pos_ptr, pos_b, gh,
+                                    gw, _INT3(*o, *(0,) * (3 - len(o))), scale, inverse, _stream(stream)), "salad_rope")
     return ys
 
 
@@ -709,14 +720,16 @@ def _rows_of(x):
 
 def _ckpt_call(fn, name, xs, cks, fmt, stream):
     """One launch for tensors of the same layout, else one each."""
-    lay = [_rows_of(x) for x in xs]
-    same = all(y[:2] == lay[0][:2] and x.dtype == xs[0].dtype for x, y in zip(xs, lay)) and len(xs) <= 4
-    for part in ([range(len(xs))] if same else [[i] for i in range(len(xs))]):
-        arr = (_CkptTensor * len(part))(*(
-            _CkptTensor(xs[i].data_ptr(), lay[i][2], cks[i].codes.data_ptr(), cks[i].scales.data_ptr()) for i in part))
-        rows, cols, _ = lay[part[0]]
-        if rows and cols:
-            _check(fn(arr, len(part), rows, cols, _TYPES[xs[part[0]].dtype], _FORMATS[fmt], _stream(stream)), name)
+    groups = {}
+    for x, c in zip(xs, cks):
+        if x.numel():
+            rows, cols, stride = _rows_of(x)
+            groups.setdefault((rows, cols, x.dtype), []).append(
+                _CKPT_TENSOR(x.data_ptr(), stride, c.codes.data_ptr(), c.scales.data_ptr()))
+    s = _stream(stream)
+    for (rows, cols, dtype), packed in groups.items():
+        for i in range(0, len(packed), 4):
+            _check(fn(b"".join(packed[i:i + 4]), len(packed[i:i + 4]), rows, cols, _TYPES[dtype], _FORMATS[fmt], s), name)
 
 
 def _ckpt_scales_shape(shape):
@@ -731,56 +744,60 @@ def ckpt_pack(x, fmt: str = "int8", out=None, stream=None):
     earlier checkpoints' memory."""
     if fmt not in _FORMATS:
         raise ValueError(f"unknown format {fmt!r}")
-    xs = list(x) if isinstance(x, (list, tuple)) else [x]
-    outs = [None] * len(xs) if out is None else list(out) if isinstance(out, (list, tuple)) else [out]
+    many = isinstance(x, (list, tuple))
+    xs = x if many else (x,)
+    outs = (None,) * len(xs) if out is None else out if many else (out,)
     if not xs or len(outs) != len(xs):
         raise ValueError("one output for each tensor")
-    for t in xs:
-        if not isinstance(t, torch.Tensor) or t.dtype not in _TYPES or t.dim() < 1:
-            raise TypeError("tensors of fp32, bf16 or fp16 with one dimension at least")
-    ctx, dev = _on(*xs)
+    ctx, _ = _on(*xs)
+    res = []
     with ctx:
-        for i, t in enumerate(xs):
-            if outs[i] is None:
-                outs[i] = Checkpoint(torch.empty(t.shape, dtype=torch.uint8, device=dev),
-                                     torch.empty(_ckpt_scales_shape(t.shape), dtype=torch.uint8, device=dev), fmt, t.dtype)
-            c = outs[i]
-            if c.codes.shape != t.shape or c.scales.shape != _ckpt_scales_shape(t.shape):
-                raise ValueError("the checkpoint's memory has another shape")
-            _dev_ptr(c.codes, torch.uint8, "codes"), _dev_ptr(c.scales, torch.uint8, "scales"), _on(t, c.codes, c.scales)
-            c.fmt, c.dtype = fmt, t.dtype
-        live = [i for i, t in enumerate(xs) if t.numel()]
-        if live:
-            _ckpt_call(lib().salad_ckpt_pack, "salad_ckpt_pack", [xs[i] for i in live], [outs[i] for i in live], fmt, stream)
-    return outs if isinstance(x, (list, tuple)) else outs[0]
+        for t, c in zip(xs, outs):
+            if t.dtype not in _TYPES or t.dim() < 1:
+                raise TypeError("tensors of fp32, bf16 or fp16 with one dimension at least")
+            scales = _ckpt_scales_shape(t.shape)
+            if c is None:
+                c = Checkpoint(t.new_empty(t.shape, dtype=torch.uint8), t.new_empty(scales, dtype=torch.uint8), fmt, t.dtype)
+            else:
+                if c.codes.shape != t.shape or c.scales.shape != scales:
+                    raise ValueError("the checkpoint's memory has another shape")
+                _on(t, c.codes, c.scales)
+                _dev_ptr(c.codes, torch.uint8, "codes"), _dev_ptr(c.scales, torch.uint8, "scales")
+                c.fmt, c.dtype = fmt, t.dtype
+            res.append(c)
+        _ckpt_call(lib().salad_ckpt_pack, "salad_ckpt_pack", xs, res, fmt, stream)
+    return res if many else res[0]
 
 
 def ckpt_unpack(ckpt, dtype=None, out=None, stream=None):
     """The values of a Checkpoint, or of each of a list, in `dtype` (by default the
     packed tensor's); exact for bf16 and fp32."""
-    cks = list(ckpt) if isinstance(ckpt, (list, tuple)) else [ckpt]
-    outs = [None] * len(cks) if out is None else list(out) if isinstance(out, (list, tuple)) else [out]
+    many = isinstance(ckpt, (list, tuple))
+    cks = ckpt if many else (ckpt,)
+    outs = (None,) * len(cks) if out is None else out if many else (out,)
     if not cks or len(outs) != len(cks):
         raise ValueError("one output for each checkpoint")
-    if any(c.fmt != cks[0].fmt or c.fmt not in _FORMATS for c in cks):
+    fmt = cks[0].fmt
+    if fmt not in _FORMATS or any(c.fmt != fmt for c in cks):
         raise ValueError("the checkpoints have several formats")
-    ctx, dev = _on(*(c.codes for c in cks), *(c.scales for c in cks))
+    ctx, _ = _on(*(t for c in cks for t in (c.codes, c.scales)))
+    res = []
     with ctx:
-        for i, c in enumerate(cks):
+        for c, y in zip(cks, outs):
             _dev_ptr(c.codes, torch.uint8, "codes"), _dev_ptr(c.scales, torch.uint8, "scales")
             if c.scales.shape != _ckpt_scales_shape(c.codes.shape):
                 raise ValueError("scales and codes have shapes that do not agree")
-            if outs[i] is None:
-                outs[i] = torch.empty(c.codes.shape, dtype=dtype or c.dtype, device=dev)
-            if outs[i].shape != c.codes.shape or outs[i].device != dev:
-                raise ValueError("the output has another shape or device")
-            if outs[i].dtype not in _TYPES or (dtype is not None and outs[i].dtype != dtype):
+            if y is None:
+                y = c.codes.new_empty(c.codes.shape, dtype=dtype or c.dtype)
+            else:
+                _on(c.codes, y)
+            if y.shape != c.codes.shape:
+                raise ValueError("the output has another shape")
+            if y.dtype not in _TYPES or (dtype is not None and y.dtype != dtype):
                 raise TypeError("outputs of fp32, bf16 or fp16, as asked for")
-        live = [i for i, c in enumerate(cks) if c.codes.numel()]
-        if live:
-            _ckpt_call(lib().salad_ckpt_unpack, "salad_ckpt_unpack", [outs[i] for i in live], [cks[i] for i in live],
-                       cks[0].fmt, stream)
-    return outs if isinstance(ckpt, (list, tuple)) else outs[0]
+            res.append(y)
+        _ckpt_call(lib().salad_ckpt_unpack, "salad_ckpt_unpack", res, cks, fmt, stream)
+    return res if many else res[0]
 
 
 def new_ckpt_backward_workspace(B: int, N: int, heads: int, d: int, device=None) -> torch.Tensor:

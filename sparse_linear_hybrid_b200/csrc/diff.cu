@@ -7,7 +7,7 @@
 // tiles; both maps read the same K and V tiles.
 //
 // Tensor memory (512 columns): S_1 [0,128), S_2 [128,256), O_1 [256,256+d),
-// O_2 [384,384+d); P_m as bf16 over the first 64 columns of S_m, so S_m of the
+// O_2 [384,384+d); P_m as bf16 over the last 64 columns of S_m, so S_m of the
 // next tile follows P_m V in the issue order.  The maps alternate: while the four
 // softmax warps of map 1 work, the tensor cores run P_2 V and S_2 of the next
 // tile, and the other way round.
@@ -71,6 +71,15 @@ __device__ __forceinline__ void diff_timeout(DiffShared* sh, uint32_t* status) {
 
 __device__ __forceinline__ float lambda_of(const void* lam, int bf16, int h) {
   return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(lam)[h] << 16) : static_cast<const float*>(lam)[h];
+}
+
+// -inf in place of the scores from column `valid` on.
+__device__ __forceinline__ void mask_keys(uint32_t (&sr)[64], int valid) {
+  if (valid < 64) {
+#pragma unroll
+    for (int i = 0; i < 64; ++i)
+      if (i >= valid) sr[i] = __float_as_uint(-INFINITY);
+  }
 }
 
 // TRAIN: also O_2 / l_2 and the log-sum-exps of both maps.
@@ -174,7 +183,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
         const uint32_t vt = sbase + C::OFF_V + (j % C::STAGES) * C::TILE;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_bf16_ts(tmem + C::TM_O + 128 * m, tmem + C::TM_S + 128 * m + kk * 8,
+          mma_bf16_ts(tmem + C::TM_O + 128 * m, tmem + C::TM_S + 128 * m + 64 + kk * 8,
                       sw128_desc(vt + kk * 2048, 16384, 1024), C::IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
       };
       auto wait_k = [&](int j) {
@@ -224,22 +233,23 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       const int valid = N - col_idx[c0 + j] * 128;  // real keys of the tile
       if (!mbar_wait_warp(&sh->s_full[m], (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
       tc_fence_after();
-      uint32_t sr[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
-      tmem_ld_wait();
-      if (valid < 128) {
-#pragma unroll
-        for (int i = 0; i < 128; ++i)
-          if (i >= valid) sr[i] = __float_as_uint(-INFINITY);
-      }
+      // The row's maximum.  The second half of the scores stays in registers, the
+      // first is read again below: all 128 at once would not leave enough for the rest.
+      uint32_t sr[64];
       float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 128; i += 8) {
-        m0 = fmax3(m0, __uint_as_float(sr[i + 0]), __uint_as_float(sr[i + 1]));
-        m1 = fmax3(m1, __uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3]));
-        m2 = fmax3(m2, __uint_as_float(sr[i + 4]), __uint_as_float(sr[i + 5]));
-        m3 = fmax3(m3, __uint_as_float(sr[i + 6]), __uint_as_float(sr[i + 7]));
+      for (int hf = 0; hf < 2; ++hf) {
+        tmem_ld32(s_addr + 64 * hf, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+        tmem_ld32(s_addr + 64 * hf + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+        tmem_ld_wait();
+        mask_keys(sr, valid - 64 * hf);
+#pragma unroll
+        for (int i = 0; i < 64; i += 8) {
+          m0 = fmax3(m0, __uint_as_float(sr[i + 0]), __uint_as_float(sr[i + 1]));
+          m1 = fmax3(m1, __uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3]));
+          m2 = fmax3(m2, __uint_as_float(sr[i + 4]), __uint_as_float(sr[i + 5]));
+          m3 = fmax3(m3, __uint_as_float(sr[i + 6]), __uint_as_float(sr[i + 7]));
+        }
       }
       const float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
       float alpha = 1.f;
@@ -266,12 +276,17 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       const uint64_t nmb2 = f32x2_pack(-m_ref * scale_log2, -m_ref * scale_log2);
       uint64_t acc0 = 0, acc1 = 0, acce = 0;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
+      for (int hf = 1; hf >= 0; --hf) {
+        if (hf == 0) {
+          tmem_ld32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+          tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+          tmem_ld_wait();
+          mask_keys(sr, valid);
+        }
+        uint32_t pk[32];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int e = 32 * c + 2 * i;
-          const uint64_t x = f32x2_fma(f32x2_pack(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2, nmb2);
+        for (int i = 0; i < 32; ++i) {
+          const uint64_t x = f32x2_fma(f32x2_pack(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), c2, nmb2);
           float p0, p1;
           if ((i & 3) == 3) {
             exp2_fma_x2(x, p0, p1);
@@ -289,7 +304,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
           else
             acc0 = f32x2_add(acc0, pp);
         }
-        tmem_st16(s_addr + 16 * c, pk);
+        tmem_st32(s_addr + 64 + 32 * hf, pk);
       }
       tmem_st_wait();
       tc_fence_before();
