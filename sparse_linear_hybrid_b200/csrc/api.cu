@@ -1173,10 +1173,13 @@ int salad_diff_backward(const void* q, const void* k, const void* v, const void*
     for (int j = 0; j < i; ++j)
       if (overlaps(made[i], bytes, made[j], bytes)) return SALAD_ERR_INVALID_ARG;
   }
-  CUtensorMap tq, tk, tv, tdo;
+  CUtensorMap tq, tk, tv, tdo, tq64, tdo64;
   if (!make_bnhd_map(&tq, q, B, N, num_heads, d, 128) || !make_bnhd_map(&tk, k, B, N, num_heads, d, 128) ||
-      !make_bnhd_map(&tv, v, B, N, num_heads, d, 128) || !make_bnhd_map(&tdo, dout, B, N, num_heads, d, 128))
+      !make_bnhd_map(&tv, v, B, N, num_heads, d, 128) || !make_bnhd_map(&tdo, dout, B, N, num_heads, d, 128) ||
+      !make_bnhd_map(&tq64, q, B, N, num_heads, d, 64) || !make_bnhd_map(&tdo64, dout, B, N, num_heads, d, 64))
     return SALAD_ERR_CUDA;
+  a.tm_q64 = &tq64;
+  a.tm_do64 = &tdo64;
   a.tm_q = &tq;
   a.tm_k = &tk;
   a.tm_v = &tv;

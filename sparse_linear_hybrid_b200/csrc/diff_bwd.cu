@@ -14,26 +14,32 @@
 //                     dS_2 as bf16 over the dP columns that the thread has read;
 //                     and the CTA's share of dlam, in fp32 from p and dp themselves
 //   diff_dkdv_kernel  one CTA per (key tile, b, h) over the query tiles that keep
-//                     it, 64 queries a step: S_1^T, S_2^T, dP^T, then (P_1 - lam
-//                     P_2)^T, dS_1^T and dS_2^T as bf16 over the scores' columns
+//                     it, 64 queries a step: S_1^T, S_2^T and dP^T are read into
+//                     registers and replaced by the next step's at once; (P_1 -
+//                     lam P_2)^T and dS_1^T go to tensor memory, dS_2^T, for which
+//                     no columns are left beside the 256 of dV and dK, to shared
+//                     memory.  The products of a step so run beside the row
+//                     warps' work on the one before and after it
 //   diff_dlam_kernel  sums the shares of every head in a fixed order
-// Gradients are rounded once, to bf16 (dlam to lam's type).  Warp roles and waits
-// as in bwd.cu.
+// Gradients are rounded once, to bf16 (dlam to lam's type).  Warp roles, 320
+// threads: warp 0 tcgen05 issuer, warp 1 TMA producer and owner of the tensor
+// memory, warps 2-9 the rows (TMEM lane quarter = warp % 4).  Every barrier wait
+// is bounded; on a time-out the kernel records it and drains.
 #include "internal.h"
 #include "ptx.cuh"
 
 namespace salad {
 namespace {
 
-constexpr int kDiffBwdThreads = 320;  // producer/issuer, TMEM owner, eight row warps
+constexpr int kDiffBwdThreads = 320;
 constexpr uint64_t kDiffBwdDrainNs = 1000000000ull;
 constexpr float kDiffLog2e = 1.4426950408889634f;
 
 struct DiffBwdShared {
   uint64_t fixed_full;
-  uint64_t ring_full[2];
-  uint64_t k_full[3], v_full[2];
-  uint64_t s_full, dp_full, s_read, ds_full, mm_done, grads_done;
+  uint64_t ring_full[4], ring_empty[4];                   // dK/dV kernel
+  uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];  // dQ kernel
+  uint64_t s_full, dp_full, s_read, ds_full, mm_done;
   uint64_t drain;
   uint32_t tmem_base;
   volatile int abort_flag;
@@ -51,11 +57,14 @@ struct DiffBwdCfg {
   static constexpr int DQ_OFF_BAR = 7 * TILE;
   static constexpr int DQ_USED = DQ_OFF_BAR + (int)sizeof(DiffBwdShared) + 1024;
   static constexpr int DQ_SMEM = DQ_USED > 122880 ? DQ_USED : 122880;
-  // dK/dV kernel: two stages of Q, dO and the four row vectors
-  static constexpr int VEC = 4 * 128 * 4;
+  // dK/dV kernel: four stages of 64 rows of Q, dO and the four row vectors; dS_2^T
+  static constexpr int HALF = 64 * D * 2;  // DCH chunks of 8 KB
+  static constexpr int STAGES = 4;
+  static constexpr int VEC = 4 * 64 * 4;
   static constexpr int OFF_RING = 2 * TILE;
-  static constexpr int OFF_VEC = 6 * TILE;
-  static constexpr int OFF_BAR = OFF_VEC + 2 * VEC;
+  static constexpr int OFF_DS = OFF_RING + STAGES * 2 * HALF;
+  static constexpr int OFF_VEC = OFF_DS + 16384;
+  static constexpr int OFF_BAR = OFF_VEC + STAGES * VEC;
   static constexpr int USED = OFF_BAR + (int)sizeof(DiffBwdShared) + 1024;
   static constexpr int SMEM = USED > 122880 ? USED : 122880;
   static constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false);
@@ -73,15 +82,16 @@ __device__ __forceinline__ float diff_lambda(const void* lam, int bf16, int h) {
   return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(lam)[h] << 16) : static_cast<const float*>(lam)[h];
 }
 
-// K-steps [first, first + count) of X Y^T (both K-major, 128-byte rows in 64-feature chunks of
-// `chunk` bytes) into D; the first one overwrites.
+// K-steps [first, first + count) of X Y^T into D, both K-major: 128-byte rows in
+// 64-feature chunks, X's of 128 rows, Y's of y_chunk bytes; the first one overwrites.
 template <int COUNT>
-__device__ __forceinline__ void mma_steps(uint32_t d_tmem, uint32_t x, uint32_t y, int first, uint32_t idesc) {
+__device__ __forceinline__ void mma_steps(uint32_t d_tmem, uint32_t x, uint32_t y, int first, uint32_t idesc,
+                                          int y_chunk = 16384) {
 #pragma unroll
   for (int i = 0; i < COUNT; ++i) {
     const int f = first + i;
-    const uint32_t off = (f / 4) * 16384 + (f % 4) * 32;
-    mma_bf16_ss(d_tmem, sw128_desc(x + off, 16, 1024), sw128_desc(y + off, 16, 1024), idesc, i > 0 ? 1u : 0u);
+    mma_bf16_ss(d_tmem, sw128_desc(x + (f / 4) * 16384 + (f % 4) * 32, 16, 1024),
+                sw128_desc(y + (f / 4) * y_chunk + (f % 4) * 32, 16, 1024), idesc, i > 0 ? 1u : 0u);
   }
 }
 
@@ -127,12 +137,11 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// p = 2^(s c - l) for 32 scores of a row, 0 from column `valid` on.
-__device__ __forceinline__ void diff_exp32(const uint32_t (&sr)[32], float c, float l, int valid, float* p) {
-  const uint64_t c2 = f32x2_pack(c, c), nl = f32x2_pack(-l, -l);
+// s <- 2^(s c - l) for 32 scores of a row, 0 from column `valid` on.
+__device__ __forceinline__ void diff_exp32(uint32_t (&s)[32], uint64_t c2, uint64_t nl, int valid) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const uint64_t x = f32x2_fma(f32x2_pack(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), c2, nl);
+    const uint64_t x = f32x2_fma(f32x2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, nl);
     float p0, p1;
     if ((i & 3) == 3) {
       exp2_fma_x2(x, p0, p1);
@@ -142,9 +151,22 @@ __device__ __forceinline__ void diff_exp32(const uint32_t (&sr)[32], float c, fl
       p0 = ex2_approx(x0);
       p1 = ex2_approx(x1);
     }
-    p[2 * i] = 2 * i < valid ? p0 : 0.f;
-    p[2 * i + 1] = 2 * i + 1 < valid ? p1 : 0.f;
+    s[2 * i] = __float_as_uint(p0);
+    s[2 * i + 1] = __float_as_uint(p1);
   }
+  if (valid < 32) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i >= valid) s[i] = 0u;
+  }
+}
+__device__ __forceinline__ uint64_t pair_of(const uint32_t (&s)[32], int i) {
+  return f32x2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+}
+__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
+  float a, b;
+  f32x2_unpack(v, a, b);
+  return pack_bf16x2(a, b);
 }
 
 // 32 fp32 columns of tensor memory times mul, as bf16 to 64 bytes of global memory.
@@ -186,8 +208,8 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(&sh->fixed_full, 1);
-    for (int st = 0; st < 3; ++st) mbar_init(&sh->k_full[st], 1);
-    for (int st = 0; st < 2; ++st) mbar_init(&sh->v_full[st], 1);
+    for (int st = 0; st < 3; ++st) mbar_init(&sh->k_full[st], 1), mbar_init(&sh->k_empty[st], 1);
+    for (int st = 0; st < 2; ++st) mbar_init(&sh->v_full[st], 1), mbar_init(&sh->v_empty[st], 1);
     mbar_init(&sh->dp_full, 1);
     mbar_init(&sh->s_full, 1);
     mbar_init(&sh->s_read, 8);
@@ -207,28 +229,44 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
   const uint32_t tmem = sh->tmem_base;
   const uint32_t q_s = sbase + C::OFF_FIX, do_s = q_s + C::TILE;
 
-  if (warp == 0) {
+  if (warp == 1) {
+    // ---------------------------------------------------------- TMA producer
     if (lane == 0) {
       bool ok = true;
       int kl = 0, vl = 0;  // K and V loads issued
-      auto load_k = [&](int j) {
-        const int st = j % 3, col = col_idx[c0 + j];
-        mbar_arrive_expect_tx(&sh->k_full[st], C::TILE);
+      mbar_arrive_expect_tx(&sh->fixed_full, 2 * C::TILE);
+#pragma unroll
+      for (int ch = 0; ch < C::DCH; ++ch) {
+        tma_load_3d(smem + C::OFF_FIX + ch * 16384, &tm_q, &sh->fixed_full, h * D + ch * 64, qt * 128, b);
+        tma_load_3d(smem + C::OFF_FIX + C::TILE + ch * 16384, &tm_do, &sh->fixed_full, h * D + ch * 64, qt * 128, b);
+      }
+      // K_j is free once the gradient products of tile j have read it, V_j once dP_j is done
+      for (int j = 0; j < n; ++j) {
+        const int col = col_idx[c0 + j], ks = j % 3, vs = j & 1;
+        if (sh->abort_flag || !mbar_wait(&sh->k_empty[ks], (uint32_t)((j / 3) & 1) ^ 1, limit_ns)) { ok = false; break; }
+        mbar_arrive_expect_tx(&sh->k_full[ks], C::TILE);
 #pragma unroll
         for (int ch = 0; ch < C::DCH; ++ch)
-          tma_load_3d(smem + C::DQ_OFF_K + st * C::TILE + ch * 16384, &tm_k, &sh->k_full[st], h * D + ch * 64,
-                      col * 128, b);
+          tma_load_3d(smem + C::DQ_OFF_K + ks * C::TILE + ch * 16384, &tm_k, &sh->k_full[ks], h * D + ch * 64, col * 128, b);
         ++kl;
-      };
-      auto load_v = [&](int j) {
-        const int st = j & 1, col = col_idx[c0 + j];
-        mbar_arrive_expect_tx(&sh->v_full[st], C::TILE);
+        if (sh->abort_flag || !mbar_wait(&sh->v_empty[vs], (uint32_t)((j >> 1) & 1) ^ 1, limit_ns)) { ok = false; break; }
+        mbar_arrive_expect_tx(&sh->v_full[vs], C::TILE);
 #pragma unroll
         for (int ch = 0; ch < C::DCH; ++ch)
-          tma_load_3d(smem + C::DQ_OFF_V + st * C::TILE + ch * 16384, &tm_v, &sh->v_full[st], h * D + ch * 64,
-                      col * 128, b);
+          tma_load_3d(smem + C::DQ_OFF_V + vs * C::TILE + ch * 16384, &tm_v, &sh->v_full[vs], h * D + ch * 64, col * 128, b);
         ++vl;
-      };
+      }
+      if (!ok) diff_bwd_timeout(sh, status);
+      // every copy this thread started lands before the CTA exits
+      mbar_wait(&sh->fixed_full, 0, kDiffBwdDrainNs);
+      for (int i = (kl > 3 ? kl - 3 : 0); i < kl; ++i)
+        mbar_wait(&sh->k_full[i % 3], (uint32_t)((i / 3) & 1), kDiffBwdDrainNs);
+      for (int i = (vl > 2 ? vl - 2 : 0); i < vl; ++i)
+        mbar_wait(&sh->v_full[i & 1], (uint32_t)((i >> 1) & 1), kDiffBwdDrainNs);
+    }
+  } else if (warp == 0) {
+    // ---------------------------------------------------------- tcgen05 issuer
+    if (lane == 0 && n > 0) {
       auto k_tile = [&](int j) { return sbase + C::DQ_OFF_K + (j % 3) * C::TILE; };
       auto v_tile = [&](int j) { return sbase + C::DQ_OFF_V + (j & 1) * C::TILE; };
       auto wait_k = [&](int j) { return mbar_wait(&sh->k_full[j % 3], (uint32_t)((j / 3) & 1), limit_ns); };
@@ -241,31 +279,20 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       auto issue_dp = [&](int j) {
         mma_steps<D / 16>(tmem + TM_DP, do_s, v_tile(j), 0, C::IDESC_S);
         mma_commit(&sh->dp_full);
+        mma_commit(&sh->v_empty[j & 1]);
       };
-      mbar_arrive_expect_tx(&sh->fixed_full, 2 * C::TILE);
-#pragma unroll
-      for (int ch = 0; ch < C::DCH; ++ch) {
-        tma_load_3d(smem + C::OFF_FIX + ch * 16384, &tm_q, &sh->fixed_full, h * D + ch * 64, qt * 128, b);
-        tma_load_3d(smem + C::OFF_FIX + C::TILE + ch * 16384, &tm_do, &sh->fixed_full, h * D + ch * 64, qt * 128, b);
-      }
-      for (int j = 0; j < n && j < 3; ++j) load_k(j);
-      for (int j = 0; j < n && j < 2; ++j) load_v(j);
       // S of the next tile as soon as the row warps hold S in registers; then the
       // gradient products and, behind them in the issue order, dP of the next
-      // tile over dS.  K_{j+3} refills K_j's stage once the gradient products
-      // have read it, V_{j+2} V_j's once dP_j is done.
-      ok = mbar_wait(&sh->fixed_full, 0, limit_ns);
-      if (ok && n >= 1) {
-        ok = wait_k(0) && wait_v(0);
-        if (ok) {
-          tc_fence_after();
-          issue_s(0);
-          issue_dp(0);
-        }
+      // tile over dS.
+      bool ok = mbar_wait(&sh->fixed_full, 0, limit_ns) && wait_k(0) && wait_v(0);
+      if (ok) {
+        tc_fence_after();
+        issue_s(0);
+        issue_dp(0);
       }
       for (int j = 0; ok && j < n; ++j) {
         if (j + 1 < n) {
-          if (sh->abort_flag || !mbar_wait(&sh->s_read, (uint32_t)(j & 1), limit_ns) || !wait_k(j + 1)) {
+          if (sh->abort_flag || !wait_k(j + 1) || !mbar_wait(&sh->s_read, (uint32_t)(j & 1), limit_ns)) {
             ok = false;
             break;
           }
@@ -281,29 +308,18 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
             mma_bf16_ts(tmem + TM_DQ + 64 * m, tmem + TM_DP + 64 * (kk >> 2) + 32 * m + 8 * (kk & 3),
                         sw128_desc(k_tile(j) + (C::DCH == 2 ? m * 16384 : 0) + kk * 2048, 16384, 1024), C::IDESC_H,
                         (j > 0 || kk > 0) ? 1u : 0u);
-        mma_commit(&sh->mm_done);
-        // dP_j completed before the row warps formed dS_j: V_j's stage is free
-        if (j + 2 < n) load_v(j + 2);
+        mma_commit(&sh->k_empty[j % 3]);
+        if (j + 1 == n) mma_commit(&sh->mm_done);
         if (j + 1 < n) {
           if (!wait_v(j + 1)) { ok = false; break; }
           tc_fence_after();
           issue_dp(j + 1);
-        }
-        if (j + 3 < n) {
-          if (!mbar_wait(&sh->mm_done, (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
-          load_k(j + 3);
         }
       }
       if (!ok) diff_bwd_timeout(sh, status);
       // every product has ended before the tensor memory is given back, also when a row warp gave up
       mma_commit(&sh->drain);
       mbar_wait(&sh->drain, 0, kDiffBwdDrainNs);
-      // every copy this thread started lands before the CTA exits
-      mbar_wait(&sh->fixed_full, 0, kDiffBwdDrainNs);
-      for (int i = (kl > 3 ? kl - 3 : 0); i < kl; ++i)
-        mbar_wait(&sh->k_full[i % 3], (uint32_t)((i / 3) & 1), kDiffBwdDrainNs);
-      for (int i = (vl > 2 ? vl - 2 : 0); i < vl; ++i)
-        mbar_wait(&sh->v_full[i & 1], (uint32_t)((i >> 1) & 1), kDiffBwdDrainNs);
     }
   } else if (warp >= 2) {
     // one thread a query row and half of the keys of every tile
@@ -311,53 +327,66 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
     const size_t total = (size_t)(gridDim.x / nb) * npad, at = (size_t)bh * npad + qt * 128 + r;
     const float l1 = rows[at], l2 = rows[total + at], D1 = rows[2 * total + at], D2 = rows[3 * total + at];
-    float dl = 0.f;
+    const uint64_t c2 = f32x2_pack(scale_log2, scale_log2), nl1 = f32x2_pack(-l1, -l1), nl2 = f32x2_pack(-l2, -l2);
+    const uint64_t nd1 = f32x2_pack(-D1, -D1), nd2 = f32x2_pack(-D2, -D2);
+    uint64_t dl2 = 0;  // (0, 0)
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const int valid = N - col_idx[c0 + j] * 128 - 64 * half;  // real keys from this half's first on
       if (!mbar_wait_warp(&sh->s_full, (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
       tc_fence_after();
-      float p1[64], p2[64];
+      // P_1, then P_2: S is released once both are in registers, so that S of the
+      // next tile runs beside P_2's exponentials
+      uint32_t p1[2][32], p2[2][32];
+      tmem_ld32(lane_addr + TM_S + 64 * half, p1[0]);
+      tmem_ld32(lane_addr + TM_S + 64 * half + 32, p1[1]);
+      tmem_ld_wait();
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t s1[32], s2[32];
-        tmem_ld32(lane_addr + TM_S + 64 * half + 32 * c, s1);
-        tmem_ld32(lane_addr + TM_S + 128 + 64 * half + 32 * c, s2);
-        tmem_ld_wait();
-        diff_exp32(s1, scale_log2, l1, valid - 32 * c, p1 + 32 * c);
-        diff_exp32(s2, scale_log2, l2, valid - 32 * c, p2 + 32 * c);
-      }
+      for (int c = 0; c < 2; ++c) diff_exp32(p1[c], c2, nl1, valid - 32 * c);
+      tmem_ld32(lane_addr + TM_S + 128 + 64 * half, p2[0]);
+      tmem_ld32(lane_addr + TM_S + 128 + 64 * half + 32, p2[1]);
+      tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->s_read);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) diff_exp32(p2[c], c2, nl2, valid - 32 * c);
       if (!mbar_wait_warp(&sh->dp_full, (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
       tc_fence_after();
+      // (both chunks of a thread's dP are read before dS takes their place: the
+      // first chunk's dS_1 lies over the first chunk, its dS_2 over the second)
+      uint32_t a[2][16];
       {
-        uint32_t pr[2][32];
-        tmem_ld32(lane_addr + TM_DP + 64 * half, pr[0]);
-        tmem_ld32(lane_addr + TM_DP + 64 * half + 32, pr[1]);
+        uint32_t g[32];
+        tmem_ld32(lane_addr + TM_DP + 64 * half, g);
         tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t a[16], z[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int e = 32 * c + 2 * i;
-            const float g0 = __uint_as_float(pr[c][2 * i]), g1 = __uint_as_float(pr[c][2 * i + 1]);
-            a[i] = pack_bf16x2(p1[e] * (g0 - D1), p1[e + 1] * (g1 - D1));
-            z[i] = pack_bf16x2(p2[e] * (g0 - D2), p2[e + 1] * (g1 - D2));
-            dl = fmaf(p2[e], g0, fmaf(p2[e + 1], g1, dl));
-          }
-          tmem_st16(lane_addr + TM_DP + 64 * half + 16 * c, a);
-          tmem_st16(lane_addr + TM_DP + 64 * half + 32 + 16 * c, z);
+        for (int i = 0; i < 16; ++i) {
+          const uint64_t gi = pair_of(g, i);
+          a[0][i] = pack_pair(f32x2_mul(pair_of(p1[0], i), f32x2_add(gi, nd1)));
+          a[1][i] = pack_pair(f32x2_mul(pair_of(p2[0], i), f32x2_add(gi, nd2)));
+          dl2 = f32x2_fma(pair_of(p2[0], i), gi, dl2);
         }
+        tmem_ld32(lane_addr + TM_DP + 64 * half + 32, g);
+        tmem_ld_wait();
+        tmem_st16(lane_addr + TM_DP + 64 * half, a[0]);
+        tmem_st16(lane_addr + TM_DP + 64 * half + 32, a[1]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint64_t gi = pair_of(g, i);
+          a[0][i] = pack_pair(f32x2_mul(pair_of(p1[1], i), f32x2_add(gi, nd1)));
+          a[1][i] = pack_pair(f32x2_mul(pair_of(p2[1], i), f32x2_add(gi, nd2)));
+          dl2 = f32x2_fma(pair_of(p2[1], i), gi, dl2);
+        }
+        tmem_st16(lane_addr + TM_DP + 64 * half + 16, a[0]);
+        tmem_st16(lane_addr + TM_DP + 64 * half + 48, a[1]);
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->ds_full);
     }
-    if (ok && n >= 1) ok = mbar_wait_warp(&sh->mm_done, (uint32_t)((n - 1) & 1), limit_ns);
+    if (ok && n >= 1) ok = mbar_wait_warp(&sh->mm_done, 0, limit_ns);  // the last gradient products
     if (!ok) {
       diff_bwd_timeout(sh, status);
     } else {
@@ -378,6 +407,9 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
         if (row < N) store_bf16_32(dst + 32 * c, g, n >= 1 ? mul : 0.f);
       }
     }
+    float dl, dl_odd;
+    f32x2_unpack(dl2, dl, dl_odd);
+    dl += dl_odd;
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) dl += __shfl_xor_sync(0xffffffffu, dl, o);
     if (lane == 0) sh->part[warp - 2] = dl;
@@ -406,12 +438,12 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
                      uint16_t* __restrict__ dk, uint16_t* __restrict__ dv, int N, int heads, int nb, int npad,
                      int mask_per_bh, float scale, float scale_log2, uint32_t* status, uint64_t limit_ns) {
   using C = DiffBwdCfg<D>;
-  // 64 queries a step.  S_1^T [0,64), S_2^T [64,128), dP^T [128,192); a thread's
-  // half e of the queries is columns [32 e, +32) of each, and it writes (P_1 - lam
-  // P_2)^T at [32 e, +16), dS_1^T at [32 e + 16, +16) and dS_2^T at [64 + 32 e, +16).
-  // dV [192,192+d), dK_1 [320,384), dK_2 [384,448) (at d = 64 both halves of q,
-  // as in the dQ kernel).
-  constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 192, TM_DK = 320;
+  // 64 queries a step.  S_1^T [0,64), S_2^T [64,128), dP^T [128,192), dV
+  // [192,192+d), dK_1 [320,384), dK_2 [384,448) (at d = 64 both halves of q, as in
+  // the dQ kernel), (P_1 - lam P_2)^T [448,480) and dS_1^T [480,512) as bf16;
+  // a thread's half e of the queries is columns [32 e, +32) of the scores and dP^T
+  // and [16 e, +16) of the bf16 operands.
+  constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 192, TM_DK = 320, TM_A = 448, TM_DS = 480;
   extern __shared__ uint8_t diff_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(diff_smem_raw) + 1023) & ~uintptr_t(1023));
   DiffBwdShared* sh = reinterpret_cast<DiffBwdShared*>(smem + C::OFF_BAR);
@@ -426,11 +458,10 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(&sh->fixed_full, 1);
-    mbar_init(&sh->ring_full[0], 1);
-    mbar_init(&sh->ring_full[1], 1);
+    for (int s = 0; s < C::STAGES; ++s) mbar_init(&sh->ring_full[s], 1), mbar_init(&sh->ring_empty[s], 1);
     mbar_init(&sh->s_full, 1);
+    mbar_init(&sh->s_read, 8);
     mbar_init(&sh->ds_full, 8);
-    mbar_init(&sh->grads_done, 1);
     mbar_init(&sh->mm_done, 1);
     mbar_init(&sh->drain, 1);
     sh->abort_flag = 0;
@@ -446,140 +477,167 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
   const uint32_t tmem = sh->tmem_base;
   const uint32_t k_s = sbase + C::OFF_FIX, v_s = k_s + C::TILE;
 
-  if (warp == 0) {
+  if (warp == 1) {
+    // ---------------------------------------------------------- TMA producer
     if (lane == 0) {
       bool ok = true;
       int loads = 0;
-      auto load_q = [&](int j) {
-        const int s = j & 1, qi = t_col_idx[c0 + j];
-        uint8_t* dst = smem + C::OFF_RING + s * 2 * C::TILE;
-        float* vec = reinterpret_cast<float*>(smem + C::OFF_VEC + s * C::VEC);
-        mbar_arrive_expect_tx(&sh->ring_full[s], 2 * C::TILE + C::VEC);
-#pragma unroll
-        for (int ch = 0; ch < C::DCH; ++ch) {
-          tma_load_3d(dst + ch * 16384, &tm_q, &sh->ring_full[s], h * D + ch * 64, qi * 128, b);
-          tma_load_3d(dst + C::TILE + ch * 16384, &tm_do, &sh->ring_full[s], h * D + ch * 64, qi * 128, b);
-        }
-        const size_t total = (size_t)(gridDim.x / nb) * npad, at = (size_t)bh * npad + (size_t)qi * 128;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) bulk_load(vec + 128 * i, rows + i * total + at, 512, &sh->ring_full[s]);
-        ++loads;
-      };
-      // scores and dP^T of step i (64 queries of tile i / 2)
-      auto issue_s = [&](int i) {
-        const uint32_t qs = sbase + C::OFF_RING + ((i >> 1) & 1) * 2 * C::TILE + (i & 1) * 8192;
-        mma_steps<D / 32>(tmem + TM_S, k_s, qs, 0, C::IDESC_SH);
-        mma_steps<D / 32>(tmem + TM_S + 64, k_s, qs, D / 32, C::IDESC_SH);
-        mma_steps<D / 16>(tmem + TM_DP, v_s, qs + C::TILE, 0, C::IDESC_SH);
-        mma_commit(&sh->s_full);
-      };
       mbar_arrive_expect_tx(&sh->fixed_full, 2 * C::TILE);
 #pragma unroll
       for (int ch = 0; ch < C::DCH; ++ch) {
         tma_load_3d(smem + C::OFF_FIX + ch * 16384, &tm_k, &sh->fixed_full, h * D + ch * 64, kt * 128, b);
         tma_load_3d(smem + C::OFF_FIX + C::TILE + ch * 16384, &tm_v, &sh->fixed_full, h * D + ch * 64, kt * 128, b);
       }
-      for (int j = 0; j < n && j < 2; ++j) load_q(j);
-      ok = mbar_wait(&sh->fixed_full, 0, limit_ns);
-      if (ok && n >= 1) {
-        ok = mbar_wait(&sh->ring_full[0], 0, limit_ns);
-        if (ok) {
-          tc_fence_after();
-          issue_s(0);
-        }
-      }
-      for (int i = 0; ok && i < 2 * n; ++i) {
-        const int j = i >> 1, ph = i & 1;
-        const uint32_t qs = sbase + C::OFF_RING + (j & 1) * 2 * C::TILE + ph * 8192;
-        if (sh->abort_flag || !mbar_wait(&sh->ds_full, (uint32_t)(i & 1), limit_ns)) { ok = false; break; }
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const uint32_t a = tmem + TM_S + 32 * (kk >> 1) + 8 * (kk & 1), acc = (i > 0 || kk > 0) ? 1u : 0u;
-          mma_bf16_ts(tmem + TM_DV, a, sw128_desc(qs + C::TILE + kk * 2048, 16384, 1024), C::IDESC_V, acc);
-          mma_bf16_ts(tmem + TM_DK, a + 16, sw128_desc(qs + kk * 2048, 16384, 1024), C::IDESC_H, acc);
-          mma_bf16_ts(tmem + TM_DK + 64, a + 64, sw128_desc(qs + (C::DCH == 2 ? 16384 : 0) + kk * 2048, 16384, 1024),
-                      C::IDESC_H, acc);
-        }
-        if (i + 1 == 2 * n) {
-          mma_commit(&sh->grads_done);
+      // step i: rows [64 (i & 1), + 64) of query tile i / 2, into the stage that
+      // the gradient products of step i - 4 have read
+      int qi = 0;
+      for (int i = 0; i < 2 * n; ++i) {
+        if ((i & 1) == 0) qi = t_col_idx[c0 + (i >> 1)];
+        const int s = i % C::STAGES, q0 = qi * 128 + 64 * (i & 1);
+        if (sh->abort_flag || !mbar_wait(&sh->ring_empty[s], (uint32_t)((i / C::STAGES) & 1) ^ 1, limit_ns)) {
+          ok = false;
           break;
         }
-        if (ph == 1) {
-          mma_commit(&sh->mm_done);
-          if (!mbar_wait(&sh->ring_full[(j + 1) & 1], (uint32_t)(((j + 1) >> 1) & 1), limit_ns)) { ok = false; break; }
+        uint8_t* dst = smem + C::OFF_RING + s * 2 * C::HALF;
+        float* vec = reinterpret_cast<float*>(smem + C::OFF_VEC + s * C::VEC);
+        mbar_arrive_expect_tx(&sh->ring_full[s], 2 * C::HALF + C::VEC);
+#pragma unroll
+        for (int ch = 0; ch < C::DCH; ++ch) {
+          tma_load_3d(dst + ch * 8192, &tm_q, &sh->ring_full[s], h * D + ch * 64, q0, b);
+          tma_load_3d(dst + C::HALF + ch * 8192, &tm_do, &sh->ring_full[s], h * D + ch * 64, q0, b);
+        }
+        const size_t total = (size_t)(gridDim.x / nb) * npad, at = (size_t)bh * npad + (size_t)q0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) bulk_load(vec + 64 * x, rows + x * total + at, 256, &sh->ring_full[s]);
+        ++loads;
+      }
+      if (!ok) diff_bwd_timeout(sh, status);
+      // every copy this thread started lands before the CTA exits
+      mbar_wait(&sh->fixed_full, 0, kDiffBwdDrainNs);
+      for (int i = (loads > C::STAGES ? loads - C::STAGES : 0); i < loads; ++i)
+        mbar_wait(&sh->ring_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), kDiffBwdDrainNs);
+    }
+  } else if (warp == 0) {
+    // ---------------------------------------------------------- tcgen05 issuer
+    if (lane == 0 && n > 0) {
+      auto stage = [&](int i) { return sbase + C::OFF_RING + (i % C::STAGES) * 2 * C::HALF; };
+      auto wait_q = [&](int i) {
+        return mbar_wait(&sh->ring_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), limit_ns);
+      };
+      auto issue_s = [&](int i) {
+        const uint32_t qs = stage(i);
+        mma_steps<D / 32>(tmem + TM_S, k_s, qs, 0, C::IDESC_SH, 8192);
+        mma_steps<D / 32>(tmem + TM_S + 64, k_s, qs, D / 32, C::IDESC_SH, 8192);
+        mma_steps<D / 16>(tmem + TM_DP, v_s, qs + C::HALF, 0, C::IDESC_SH, 8192);
+        mma_commit(&sh->s_full);
+      };
+      const int steps = 2 * n;
+      bool ok = mbar_wait(&sh->fixed_full, 0, limit_ns) && wait_q(0);
+      if (ok) {
+        tc_fence_after();
+        issue_s(0);
+      }
+      // Step i: the next scores as soon as this step's are in the row warps'
+      // registers, then this step's gradient products once their operands are written.
+      for (int i = 0; ok && i < steps; ++i) {
+        if (i + 1 < steps) {
+          if (sh->abort_flag || !wait_q(i + 1) || !mbar_wait(&sh->s_read, (uint32_t)(i & 1), limit_ns)) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
+          issue_s(i + 1);
         }
-        issue_s(i + 1);  // over the operands of the products before it, which run first
-        if (ph == 1 && j + 2 < n) {
-          // the stage of tile j is free once its gradient products have read it
-          if (!mbar_wait(&sh->mm_done, (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
-          load_q(j + 2);
+        if (sh->abort_flag || !mbar_wait(&sh->ds_full, (uint32_t)(i & 1), limit_ns)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t qs = stage(i), ds_s = sbase + C::OFF_DS;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint32_t acc = (i > 0 || kk > 0) ? 1u : 0u;
+          mma_bf16_ts(tmem + TM_DV, tmem + TM_A + 8 * kk, sw128_desc(qs + C::HALF + kk * 2048, 8192, 1024), C::IDESC_V, acc);
+          mma_bf16_ts(tmem + TM_DK, tmem + TM_DS + 8 * kk, sw128_desc(qs + kk * 2048, 8192, 1024), C::IDESC_H, acc);
+          mma_bf16_ss(tmem + TM_DK + 64, sw128_desc(ds_s + kk * 32, 16, 1024),
+                      sw128_desc(qs + (C::DCH == 2 ? 8192 : 0) + kk * 2048, 8192, 1024), C::IDESC_H, acc);
         }
+        mma_commit(&sh->mm_done);
+        mma_commit(&sh->ring_empty[i % C::STAGES]);
       }
       if (!ok) diff_bwd_timeout(sh, status);
       // every product has ended before the tensor memory is given back, also when a row warp gave up
       mma_commit(&sh->drain);
       mbar_wait(&sh->drain, 0, kDiffBwdDrainNs);
-      mbar_wait(&sh->fixed_full, 0, kDiffBwdDrainNs);
-      for (int i = (loads > 2 ? loads - 2 : 0); i < loads; ++i)
-        mbar_wait(&sh->ring_full[i & 1], (uint32_t)((i >> 1) & 1), kDiffBwdDrainNs);
     }
   } else if (warp >= 2) {
     // one thread a key row and half of a step's queries
     const int quarter = warp & 3, r = quarter * 32 + lane, half = (warp - 2) >> 2;
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
     const float lh = diff_lambda(lam, lam_bf16, h);
+    const uint64_t c2 = f32x2_pack(scale_log2, scale_log2), nlam = f32x2_pack(-lh, -lh);
+    const uint64_t minus = f32x2_pack(-1.f, -1.f);
     bool ok = true;
     for (int i = 0; i < 2 * n; ++i) {
-      const int j = i >> 1, s = j & 1;
+      const int s = i % C::STAGES;
       if (!mbar_wait_warp(&sh->s_full, (uint32_t)(i & 1), limit_ns) ||
-          !mbar_wait_warp(&sh->ring_full[s], (uint32_t)((j >> 1) & 1), limit_ns)) {
+          !mbar_wait_warp(&sh->ring_full[s], (uint32_t)((i / C::STAGES) & 1), limit_ns)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const float* vec = reinterpret_cast<const float*>(smem + C::OFF_VEC + s * C::VEC) + 64 * (i & 1) + 32 * half;
-      uint32_t s1[32], s2[32], pr[32];
+      const uint32_t vec = sbase + C::OFF_VEC + s * C::VEC + 128 * half;  // lse_1, then + 256 bytes lse_2, D_1, D_2
+      uint32_t s1[32], s2[32], g[32];
       tmem_ld32(lane_addr + TM_S + 32 * half, s1);
       tmem_ld32(lane_addr + TM_S + 64 + 32 * half, s2);
-      tmem_ld32(lane_addr + TM_DP + 32 * half, pr);
+      tmem_ld32(lane_addr + TM_DP + 32 * half, g);
       tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->s_read);
       uint32_t a[16], z1[16], z2[16];
-      const uint64_t c2 = f32x2_pack(scale_log2, scale_log2);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float2 la = *reinterpret_cast<const float2*>(vec + 2 * k), lb = *reinterpret_cast<const float2*>(vec + 128 + 2 * k);
-        const float2 da = *reinterpret_cast<const float2*>(vec + 256 + 2 * k), db = *reinterpret_cast<const float2*>(vec + 384 + 2 * k);
-        const uint64_t x1 = f32x2_fma(f32x2_pack(__uint_as_float(s1[2 * k]), __uint_as_float(s1[2 * k + 1])), c2, f32x2_pack(-la.x, -la.y));
-        const uint64_t x2 = f32x2_fma(f32x2_pack(__uint_as_float(s2[2 * k]), __uint_as_float(s2[2 * k + 1])), c2, f32x2_pack(-lb.x, -lb.y));
-        float p0, p1, q0, q1;
-        if ((k & 3) == 3) {
-          exp2_fma_x2(x1, p0, p1);
-          exp2_fma_x2(x2, q0, q1);
-        } else {
-          float y0, y1;
-          f32x2_unpack(x1, y0, y1);
-          p0 = ex2_approx(y0);
-          p1 = ex2_approx(y1);
-          f32x2_unpack(x2, y0, y1);
-          q0 = ex2_approx(y0);
-          q1 = ex2_approx(y1);
+      for (int k = 0; k < 16; k += 2) {
+        uint32_t w[4][4];  // the row vectors of four queries
+#pragma unroll
+        for (int x = 0; x < 4; ++x) ld_shared_v4(vec + 256 * x + 8 * k, w[x][0], w[x][1], w[x][2], w[x][3]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          auto row = [&](int x) { return f32x2_pack(__uint_as_float(w[x][2 * u]), __uint_as_float(w[x][2 * u + 1])); };
+          const uint64_t x1 = f32x2_fma(pair_of(s1, k + u), c2, f32x2_mul(row(0), minus));
+          const uint64_t x2 = f32x2_fma(pair_of(s2, k + u), c2, f32x2_mul(row(1), minus));
+          float p0, p1, q0, q1;
+          if (((k + u) & 3) == 3) {
+            exp2_fma_x2(x1, p0, p1);
+            exp2_fma_x2(x2, q0, q1);
+          } else {
+            float y0, y1;
+            f32x2_unpack(x1, y0, y1);
+            p0 = ex2_approx(y0);
+            p1 = ex2_approx(y1);
+            f32x2_unpack(x2, y0, y1);
+            q0 = ex2_approx(y0);
+            q1 = ex2_approx(y1);
+          }
+          const uint64_t p = f32x2_pack(p0, p1), q = f32x2_pack(q0, q1), gi = pair_of(g, k + u);
+          a[k + u] = pack_pair(f32x2_fma(nlam, q, p));
+          z1[k + u] = pack_pair(f32x2_mul(p, f32x2_fma(row(2), minus, gi)));
+          z2[k + u] = pack_pair(f32x2_mul(q, f32x2_fma(row(3), minus, gi)));
         }
-        const float g0 = __uint_as_float(pr[2 * k]), g1 = __uint_as_float(pr[2 * k + 1]);
-        a[k] = pack_bf16x2(fmaf(-lh, q0, p0), fmaf(-lh, q1, p1));
-        z1[k] = pack_bf16x2(p0 * (g0 - da.x), p1 * (g1 - da.y));
-        z2[k] = pack_bf16x2(q0 * (g0 - db.x), q1 * (g1 - db.y));
       }
-      tmem_st16(lane_addr + TM_S + 32 * half, a);
-      tmem_st16(lane_addr + TM_S + 32 * half + 16, z1);
-      tmem_st16(lane_addr + TM_S + 64 + 32 * half, z2);
+      // the products of the step before have read the operands' places
+      if (i >= 1 && !mbar_wait_warp(&sh->mm_done, (uint32_t)((i - 1) & 1), limit_ns)) { ok = false; break; }
+      tc_fence_after();
+      tmem_st16(lane_addr + TM_A + 16 * half, a);
+      tmem_st16(lane_addr + TM_DS + 16 * half, z1);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        st_shared_v4(sbase + C::OFF_DS + sw128_offset((uint32_t)r, (uint32_t)(4 * half + x)), z2[4 * x], z2[4 * x + 1],
+                     z2[4 * x + 2], z2[4 * x + 3]);
+      fence_proxy_async_smem();
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->ds_full);
     }
-    if (ok && n >= 1) ok = mbar_wait_warp(&sh->grads_done, 0, limit_ns);
+    if (ok && n >= 1) ok = mbar_wait_warp(&sh->mm_done, (uint32_t)((2 * n - 1) & 1), limit_ns);
     if (!ok) {
       diff_bwd_timeout(sh, status);
     } else {
@@ -656,7 +714,7 @@ cudaError_t launch_diff_bwd_t(const DiffArgs& a, cudaStream_t s) {
   e = cudaFuncSetAttribute(diff_dkdv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   diff_dkdv_kernel<D><<<grid, kDiffBwdThreads, C::SMEM, s>>>(
-      *a.tm_q, *a.tm_k, *a.tm_v, *a.tm_do, a.t_row_ptr, a.t_col_idx, a.rows, a.lam, a.lam_bf16, a.dk, a.dv, a.N,
+      *a.tm_q64, *a.tm_k, *a.tm_v, *a.tm_do64, a.t_row_ptr, a.t_col_idx, a.rows, a.lam, a.lam_bf16, a.dk, a.dv, a.N,
       a.heads, a.nb, a.npad, a.mask_per_bh, a.scale, a.scale_log2, a.status, a.wait_limit_ns);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;

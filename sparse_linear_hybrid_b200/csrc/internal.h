@@ -229,7 +229,7 @@ cudaError_t launch_narrow3(const float* x, uint16_t* y0, uint16_t* y1, uint16_t*
 struct DiffArgs {
   const CUtensorMap *tm_q, *tm_k, *tm_v;  // box (64, 128, 1)
   const CUtensorMap *tm_out, *tm_out2;    // forward (tm_out2: with lse)
-  const CUtensorMap* tm_do;               // backward
+  const CUtensorMap *tm_do, *tm_q64, *tm_do64;  // backward (boxes of 128 and of 64 rows)
   const int32_t *row_ptr, *col_idx, *t_row_ptr, *t_col_idx;
   const void* lam;                        // [heads], bf16 or fp32
   int lam_bf16;
