@@ -67,6 +67,16 @@ bool make_bnhd_map(CUtensorMap* m, const void* base, int B, int N, int Hh, int d
   return make_map(m, base, 3, dims, strides, box);
 }
 
+// [B][N][Hh][d] bf16 viewed as (64, N, Hh*d/64, B); box (64, rows, d/64, 1): one
+// copy brings all 64-feature chunks of a head's rows, one chunk after another.
+bool make_head_map(CUtensorMap* m, const void* base, int B, int N, int Hh, int d, uint32_t rows) {
+  const uint64_t row = (uint64_t)Hh * d * 2;
+  const uint64_t dims[4] = {64, (uint64_t)N, (uint64_t)Hh * d / 64, (uint64_t)B};
+  const uint64_t strides[3] = {row, 128, (uint64_t)N * row};
+  const uint32_t box[4] = {64, rows, (uint32_t)d / 64, 1};
+  return make_map(m, base, 4, dims, strides, box);
+}
+
 // [B][T][H][W][Hh][d] bf16 viewed as a 4-D tensor (Hh*d, W, H, B*T); box
 // (64, bw, bh, bt), one 3-D tile block of one head's 64-feature chunk.
 bool make_tile_map(CUtensorMap* m, const void* base, int B, const TileGeom& g, int Hh, int d) {
@@ -1134,9 +1144,9 @@ int salad_diff_forward(const void* q, const void* k, const void* v, int B, int N
       if (overlaps(made[i].p, made[i].n, made[j].p, made[j].n)) return SALAD_ERR_INVALID_ARG;
   }
   CUtensorMap tq, tk, tv, to, to2;
-  if (!make_bnhd_map(&tq, q, B, N, num_heads, d, 128) || !make_bnhd_map(&tk, k, B, N, num_heads, d, 128) ||
-      !make_bnhd_map(&tv, v, B, N, num_heads, d, 128) || !make_bnhd_map(&to, out, B, N, num_heads, d, 128) ||
-      !make_bnhd_map(&to2, out2 ? out2 : out, B, N, num_heads, d, 128))
+  if (!make_head_map(&tq, q, B, N, num_heads, d, 128) || !make_head_map(&tk, k, B, N, num_heads, d, 128) ||
+      !make_head_map(&tv, v, B, N, num_heads, d, 128) || !make_head_map(&to, out, B, N, num_heads, d, 128) ||
+      !make_head_map(&to2, out2 ? out2 : out, B, N, num_heads, d, 128))
     return SALAD_ERR_CUDA;
   a.tm_q = &tq;
   a.tm_k = &tk;
@@ -1174,9 +1184,9 @@ int salad_diff_backward(const void* q, const void* k, const void* v, const void*
       if (overlaps(made[i], bytes, made[j], bytes)) return SALAD_ERR_INVALID_ARG;
   }
   CUtensorMap tq, tk, tv, tdo, tq64, tdo64;
-  if (!make_bnhd_map(&tq, q, B, N, num_heads, d, 128) || !make_bnhd_map(&tk, k, B, N, num_heads, d, 128) ||
-      !make_bnhd_map(&tv, v, B, N, num_heads, d, 128) || !make_bnhd_map(&tdo, dout, B, N, num_heads, d, 128) ||
-      !make_bnhd_map(&tq64, q, B, N, num_heads, d, 64) || !make_bnhd_map(&tdo64, dout, B, N, num_heads, d, 64))
+  if (!make_head_map(&tq, q, B, N, num_heads, d, 128) || !make_head_map(&tk, k, B, N, num_heads, d, 128) ||
+      !make_head_map(&tv, v, B, N, num_heads, d, 128) || !make_head_map(&tdo, dout, B, N, num_heads, d, 128) ||
+      !make_head_map(&tq64, q, B, N, num_heads, d, 64) || !make_head_map(&tdo64, dout, B, N, num_heads, d, 64))
     return SALAD_ERR_CUDA;
   a.tm_q64 = &tq64;
   a.tm_do64 = &tdo64;

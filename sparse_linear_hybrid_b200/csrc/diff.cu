@@ -11,9 +11,11 @@
 // next tile follows P_m V in the issue order.  The maps alternate: while the four
 // softmax warps of map 1 work, the tensor cores run P_2 V and S_2 of the next
 // tile, and the other way round.
-// Warp roles, 320 threads: warp 0 TMA producer (K and V rings of three tiles),
-// warp 1 tcgen05 issuer and owner of the tensor memory, warps 2-5 softmax of map
-// 1 and warps 6-9 of map 2, one thread a query row.  The running maximum only
+// Warp roles, 384 threads: warp 0 TMA producer (K and V rings of three tiles),
+// warp 1 tcgen05 issuer and owner of the tensor memory, warps 4-7 softmax of map
+// 1 and warps 8-11 of map 2, one thread a query row.  Map 2's warps begin after
+// map 1's have written their first P: the two groups then stay half a tile apart,
+// one in the exponentials while the other waits for its products.  The running maximum only
 // moves (and O_m is rescaled in tensor memory) when it grows by more than 2^8.
 // The row sum adds the bf16-rounded p that the value product reads, so the
 // rounding of a dominant key cancels in O / l.  At the end the two warp groups
@@ -29,7 +31,7 @@
 namespace salad {
 namespace {
 
-constexpr int kDiffThreads = 320;
+constexpr int kDiffThreads = 384;
 constexpr uint64_t kDiffDrainNs = 1000000000ull;
 constexpr float kDiffRescale = 8.0f;  // log2 units
 constexpr float kLn2 = 0.69314718055994531f;
@@ -40,6 +42,7 @@ struct DiffShared {
   uint64_t s_full[2];   // per map: S of the current tile is in tensor memory (and the P V before it is done)
   uint64_t p_full[2];   // per map: the four softmax warps have written P
   uint64_t o_full;      // every product is done
+  uint64_t turn;        // map 1's softmax warps have written their first P
   uint64_t drain;
   uint32_t tmem_base;
   volatile int abort_flag;
@@ -116,6 +119,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       mbar_init(&sh->p_full[m], 4);
     }
     mbar_init(&sh->o_full, 1);
+    mbar_init(&sh->turn, 4);
     mbar_init(&sh->drain, 1);
     sh->abort_flag = 0;
     fence_mbar_init();
@@ -127,7 +131,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh->tmem_base;
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's: they begin at 0
 
   if (warp == 0) {
     if (lane == 0) {
@@ -136,40 +140,33 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       bool ok = true;
       int kl = 0, vl = 0;
       mbar_arrive_expect_tx(&sh->q_full, C::TILE);
-#pragma unroll
-      for (int ch = 0; ch < C::DCH; ++ch)
-        tma_load_3d(smem + C::OFF_Q + ch * 16384, &tm_q, &sh->q_full, h * D + ch * 64, qt * 128, b);
+      tma_load_4d(smem + C::OFF_Q, &tm_q, &sh->q_full, 0, qt * 128, h * C::DCH, b);
       for (int j = 0; j < n; ++j) {
         const int s = j % C::STAGES, col = col_idx[c0 + j];
         const uint32_t ph = (uint32_t)((j / C::STAGES) & 1);
-        if (sh->abort_flag || !mbar_wait(&sh->k_empty[s], ph ^ 1, limit_ns)) { ok = false; break; }
+        if (sh->abort_flag || !mbar_await(&sh->k_empty[s], ph ^ 1, limit_ns)) { ok = false; break; }
         mbar_arrive_expect_tx(&sh->k_full[s], C::TILE);
-#pragma unroll
-        for (int ch = 0; ch < C::DCH; ++ch)
-          tma_load_3d(smem + C::OFF_K + s * C::TILE + ch * 16384, &tm_k, &sh->k_full[s], h * D + ch * 64, col * 128, b);
+        tma_load_4d(smem + C::OFF_K + s * C::TILE, &tm_k, &sh->k_full[s], 0, col * 128, h * C::DCH, b);
         ++kl;
-        if (sh->abort_flag || !mbar_wait(&sh->v_empty[s], ph ^ 1, limit_ns)) { ok = false; break; }
+        if (sh->abort_flag || !mbar_await(&sh->v_empty[s], ph ^ 1, limit_ns)) { ok = false; break; }
         mbar_arrive_expect_tx(&sh->v_full[s], C::TILE);
-#pragma unroll
-        for (int ch = 0; ch < C::DCH; ++ch)
-          tma_load_3d(smem + C::OFF_V + s * C::TILE + ch * 16384, &tm_v, &sh->v_full[s], h * D + ch * 64, col * 128, b);
+        tma_load_4d(smem + C::OFF_V + s * C::TILE, &tm_v, &sh->v_full[s], 0, col * 128, h * C::DCH, b);
         ++vl;
       }
       if (!ok) diff_timeout(sh, status);
       // every copy this thread started lands before the CTA exits
-      mbar_wait(&sh->q_full, 0, kDiffDrainNs);
+      mbar_await(&sh->q_full, 0, kDiffDrainNs);
       for (int i = (kl > C::STAGES ? kl - C::STAGES : 0); i < kl; ++i)
-        mbar_wait(&sh->k_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), kDiffDrainNs);
+        mbar_await(&sh->k_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), kDiffDrainNs);
       for (int i = (vl > C::STAGES ? vl - C::STAGES : 0); i < vl; ++i)
-        mbar_wait(&sh->v_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), kDiffDrainNs);
+        mbar_await(&sh->v_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), kDiffDrainNs);
     }
   } else if (warp == 1) {
-    if (lane == 0 && n > 0) {
-      bool ok = mbar_wait(&sh->q_full, 0, limit_ns);
-      const uint32_t q_s = sbase + C::OFF_Q;
-      // S_m of tile j: the k-steps of the map's half of the features
-      auto issue_s = [&](int m, int j) {
-        const uint32_t kt = sbase + C::OFF_K + (j % C::STAGES) * C::TILE;
+    // ---------------------------------------------------------- tcgen05 issuer
+    if (n > 0) {  // (the whole warp; one lane issues)
+      // S_m from stage s: the k-steps of the map's half of the features
+      auto issue_s = [&](int m, int s) {
+        const uint32_t q_s = sbase + C::OFF_Q, kt = sbase + C::OFF_K + s * C::TILE;
 #pragma unroll
         for (int kk = 0; kk < D / 32; ++kk) {
           const int f = m * (D / 32) + kk;
@@ -178,51 +175,52 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
                       C::IDESC_S, kk > 0 ? 1u : 0u);
         }
         mma_commit(&sh->s_full[m]);
+        if (m == 1) mma_commit(&sh->k_empty[s]);
       };
-      auto issue_pv = [&](int m, int j) {
-        const uint32_t vt = sbase + C::OFF_V + (j % C::STAGES) * C::TILE;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_bf16_ts(tmem + C::TM_O + 128 * m, tmem + C::TM_S + 128 * m + 64 + kk * 8,
-                      sw128_desc(vt + kk * 2048, 16384, 1024), C::IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
-      };
-      auto wait_k = [&](int j) {
-        return mbar_wait(&sh->k_full[j % C::STAGES], (uint32_t)((j / C::STAGES) & 1), limit_ns);
-      };
-      ok = ok && wait_k(0);
+      bool ok = mbar_await_warp(&sh->q_full, 0, limit_ns) && mbar_await_warp(&sh->k_full[0], 0, limit_ns);
       if (ok) {
         tc_fence_after();
-        issue_s(0, 0);
-        issue_s(1, 0);
-        mma_commit(&sh->k_empty[0]);
-      }
-      for (int j = 0; ok && j < n; ++j) {
-        const int s = j % C::STAGES;
-        if (!mbar_wait(&sh->v_full[s], (uint32_t)((j / C::STAGES) & 1), limit_ns) || (j + 1 < n && !wait_k(j + 1))) {
-          ok = false;
-          break;
+        if (elect_one()) {
+          issue_s(0, 0);
+          issue_s(1, 0);
         }
+      }
+      int s = 0;
+      uint32_t ph = 0;  // stage and parity of tile j
+      for (int j = 0; ok && j < n; ++j) {
+        const int s1 = s + 1 == C::STAGES ? 0 : s + 1;
+        const uint32_t ph1 = s1 == 0 ? ph ^ 1 : ph;
+        ok = mbar_await_warp(&sh->v_full[s], ph, limit_ns) &&
+             (j + 1 == n || mbar_await_warp(&sh->k_full[s1], ph1, limit_ns));
+#pragma unroll
         for (int m = 0; m < 2; ++m) {
-          if (sh->abort_flag || !mbar_wait(&sh->p_full[m], (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
+          ok = ok && !__any_sync(0xffffffffu, sh->abort_flag) && mbar_await_warp(&sh->p_full[m], (uint32_t)(j & 1), limit_ns);
+          if (!ok) break;
           tc_fence_after();
-          issue_pv(m, j);
-          if (m == 1) mma_commit(&sh->v_empty[s]);
-          if (j + 1 < n) {
-            issue_s(m, j + 1);
-            if (m == 1) mma_commit(&sh->k_empty[(j + 1) % C::STAGES]);
+          if (elect_one()) {
+            const uint32_t vt = sbase + C::OFF_V + s * C::TILE;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_bf16_ts(tmem + C::TM_O + 128 * m, tmem + C::TM_S + 128 * m + 64 + kk * 8,
+                          sw128_desc(vt + kk * 2048, 16384, 1024), C::IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
+            if (m == 1) mma_commit(&sh->v_empty[s]);
+            if (j + 1 < n) issue_s(m, s1);  // over P, behind the product that reads it
           }
         }
+        s = s1;
+        ph = ph1;
       }
-      if (ok)
-        mma_commit(&sh->o_full);
-      else
+      if (ok) {
+        if (elect_one()) mma_commit(&sh->o_full);
+      } else {
         diff_timeout(sh, status);
+      }
       // every product has ended before the tensor memory is given back, also when a softmax warp gave up
-      mma_commit(&sh->drain);
-      mbar_wait(&sh->drain, 0, kDiffDrainNs);
+      if (elect_one()) mma_commit(&sh->drain);
+      mbar_await_warp(&sh->drain, 0, kDiffDrainNs);
     }
-  } else {
-    const int m = (warp - 2) >> 2;  // the map
+  } else if (warp >= 4) {
+    const int m = (warp - 4) >> 2;  // the map
     const int quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t s_addr = lane_addr + C::TM_S + 128 * m, o_addr = lane_addr + C::TM_O + 128 * m;
@@ -231,7 +229,11 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const int valid = N - col_idx[c0 + j] * 128;  // real keys of the tile
-      if (!mbar_wait_warp(&sh->s_full[m], (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
+      if (!mbar_await_warp(&sh->s_full[m], (uint32_t)(j & 1), limit_ns) ||
+          (m == 1 && j == 0 && !mbar_await_warp(&sh->turn, 0, limit_ns))) {
+        ok = false;
+        break;
+      }
       tc_fence_after();
       // The row's maximum.  The second half of the scores stays in registers, the
       // first is read again below: all 128 at once would not leave enough for the rest.
@@ -309,7 +311,10 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->p_full[m]);
+      if (lane == 0) {
+        mbar_arrive(&sh->p_full[m]);
+        if (m == 0 && j == 0) mbar_arrive(&sh->turn);
+      }
       float a0, a1;
       f32x2_unpack(f32x2_add(acc0, acc1), a0, a1);
       l = l * alpha + (a0 + a1);
@@ -318,7 +323,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
         le = le * alpha + (a0 + a1);
       }
     }
-    if (ok && n > 0) ok = mbar_wait_warp(&sh->o_full, 0, limit_ns);
+    if (ok && n > 0) ok = mbar_await_warp(&sh->o_full, 0, limit_ns);
     if (!ok) diff_timeout(sh, status);
     const int row = qt * 128 + r;
     if (TRAIN && ok && row < N) {
@@ -331,7 +336,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     // features [m D/2, m D/2 + D/2) of this row: out = O_1 / l_1 - lam O_2 / l_2
     const float lh = lambda_of(lam, lam_bf16, h);
     const float i1 = n > 0 ? 1.f / sh->sum[0][r] : 0.f, i2 = n > 0 ? 1.f / sh->sum[1][r] : 0.f;
-    if (n == 0) mbar_wait_warp(&sh->q_full, 0, limit_ns);  // the Q buffer is written over: its load must have landed
+    if (n == 0) mbar_await_warp(&sh->q_full, 0, limit_ns);  // the Q buffer is written over: its load must have landed
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       const int f0 = m * (D / 2) + 32 * c;  // 32 features
@@ -362,12 +367,9 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     }
     fence_proxy_async_smem();
     named_bar_sync(1, 256);
-    if (warp == 2 && lane == 0 && !sh->abort_flag) {
-#pragma unroll
-      for (int ch = 0; ch < C::DCH; ++ch) {
-        tma_store_3d(&tm_out, smem + C::OFF_Q + ch * 16384, h * D + ch * 64, qt * 128, b);
-        if (TRAIN) tma_store_3d(&tm_out2, smem + C::OFF_K + ch * 16384, h * D + ch * 64, qt * 128, b);
-      }
+    if (warp == 4 && lane == 0 && !sh->abort_flag) {
+      tma_store_4d(&tm_out, smem + C::OFF_Q, 0, qt * 128, h * C::DCH, b);
+      if (TRAIN) tma_store_4d(&tm_out2, smem + C::OFF_K, 0, qt * 128, h * C::DCH, b);
       bulk_commit_group();
       bulk_wait_group_read0();
     }

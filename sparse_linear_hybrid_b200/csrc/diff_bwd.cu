@@ -21,17 +21,21 @@
 //                     memory.  The products of a step so run beside the row
 //                     warps' work on the one before and after it
 //   diff_dlam_kernel  sums the shares of every head in a fixed order
-// Gradients are rounded once, to bf16 (dlam to lam's type).  Warp roles, 320
-// threads: warp 0 tcgen05 issuer, warp 1 TMA producer and owner of the tensor
-// memory, warps 2-9 the rows (TMEM lane quarter = warp % 4).  Every barrier wait
-// is bounded; on a time-out the kernel records it and drains.
+// Gradients are rounded once, to bf16 (dlam to lam's type).  Warp roles, 384
+// threads: warp 0 TMA producer, warps 1-3 tcgen05 issuers (warp 1 owns the tensor
+// memory), warps 4-11 the rows (TMEM lane quarter = warp % 4).  There are several
+// issuers because a warp that pushes products into a full tensor-core queue holds
+// up the shared-memory instructions of its scheduler's other warps: with one
+// issuer two of the eight row warps ran 500 to 900 of 2,400 cycles a step behind
+// the others (clock64).  Every barrier wait is bounded; on a time-out the kernel
+// records it and drains.
 #include "internal.h"
 #include "ptx.cuh"
 
 namespace salad {
 namespace {
 
-constexpr int kDiffBwdThreads = 320;
+constexpr int kDiffBwdThreads = 384;
 constexpr uint64_t kDiffBwdDrainNs = 1000000000ull;
 constexpr float kDiffLog2e = 1.4426950408889634f;
 
@@ -95,7 +99,8 @@ __device__ __forceinline__ void mma_steps(uint32_t d_tmem, uint32_t x, uint32_t 
   }
 }
 
-// rows[4][B*Hh][npad]: lse_1 and lse_2 (base 2; +inf in pad rows), D_1, D_2.
+// rows[B*Hh][npad/64][4][64]: lse_1 and lse_2 (base 2; +inf in pad rows), D_1, D_2
+// of 64 queries, the piece that a step of the dK/dV kernel loads.
 // D/8 lanes a row, eight features a lane.
 template <int D>
 __global__ void __launch_bounds__(256)
@@ -109,7 +114,7 @@ __global__ void __launch_bounds__(256)
   if (t >= total) return;  // (whole groups of lanes leave; total is a multiple of 128 rows, so whole CTAs do)
   // rows of neighbouring heads of a token lie side by side: h fastest
   const int h = (int)(t % heads), n = (int)(t / heads % npad), b = (int)(t / heads / npad);
-  const int64_t bh = (int64_t)b * heads + h, at = bh * npad + n;
+  const int64_t bh = (int64_t)b * heads + h;
   float d0 = 0.f, d2 = 0.f;
   if (n < N) {
     const int64_t off = (((int64_t)b * N + n) * heads + h) * D + part * 8;
@@ -130,10 +135,11 @@ __global__ void __launch_bounds__(256)
   }
   if (part == 0) {
     const int64_t BH = (int64_t)B * heads;
-    rows[at] = n < N ? lse[bh * N + n] * kDiffLog2e : INFINITY;
-    rows[total + at] = n < N ? lse[(BH + bh) * N + n] * kDiffLog2e : INFINITY;
-    rows[2 * total + at] = fmaf(diff_lambda(lam, lam_bf16, h), d2, d0);
-    rows[3 * total + at] = d2;
+    float* at = rows + bh * npad * 4 + n / 64 * 256 + n % 64;
+    at[0] = n < N ? lse[bh * N + n] * kDiffLog2e : INFINITY;
+    at[64] = n < N ? lse[(BH + bh) * N + n] * kDiffLog2e : INFINITY;
+    at[128] = fmaf(diff_lambda(lam, lam_bf16, h), d2, d0);
+    at[192] = d2;
   }
 }
 
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     mbar_init(&sh->s_read, 8);
     mbar_init(&sh->ds_full, 8);
     mbar_init(&sh->mm_done, 1);
-    mbar_init(&sh->drain, 1);
+    mbar_init(&sh->drain, 2);
     sh->abort_flag = 0;
     fence_mbar_init();
   }
@@ -226,114 +232,124 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh->tmem_base;
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's: they begin at 0
   const uint32_t q_s = sbase + C::OFF_FIX, do_s = q_s + C::TILE;
 
-  if (warp == 1) {
+  if (warp == 0) {
     // ---------------------------------------------------------- TMA producer
     if (lane == 0) {
       bool ok = true;
       int kl = 0, vl = 0;  // K and V loads issued
       mbar_arrive_expect_tx(&sh->fixed_full, 2 * C::TILE);
-#pragma unroll
-      for (int ch = 0; ch < C::DCH; ++ch) {
-        tma_load_3d(smem + C::OFF_FIX + ch * 16384, &tm_q, &sh->fixed_full, h * D + ch * 64, qt * 128, b);
-        tma_load_3d(smem + C::OFF_FIX + C::TILE + ch * 16384, &tm_do, &sh->fixed_full, h * D + ch * 64, qt * 128, b);
-      }
+      tma_load_4d(smem + C::OFF_FIX, &tm_q, &sh->fixed_full, 0, qt * 128, h * C::DCH, b);
+      tma_load_4d(smem + C::OFF_FIX + C::TILE, &tm_do, &sh->fixed_full, 0, qt * 128, h * C::DCH, b);
       // K_j is free once the gradient products of tile j have read it, V_j once dP_j is done
       for (int j = 0; j < n; ++j) {
         const int col = col_idx[c0 + j], ks = j % 3, vs = j & 1;
-        if (sh->abort_flag || !mbar_wait(&sh->k_empty[ks], (uint32_t)((j / 3) & 1) ^ 1, limit_ns)) { ok = false; break; }
+        if (sh->abort_flag || !mbar_await(&sh->k_empty[ks], (uint32_t)((j / 3) & 1) ^ 1, limit_ns)) { ok = false; break; }
         mbar_arrive_expect_tx(&sh->k_full[ks], C::TILE);
-#pragma unroll
-        for (int ch = 0; ch < C::DCH; ++ch)
-          tma_load_3d(smem + C::DQ_OFF_K + ks * C::TILE + ch * 16384, &tm_k, &sh->k_full[ks], h * D + ch * 64, col * 128, b);
+        tma_load_4d(smem + C::DQ_OFF_K + ks * C::TILE, &tm_k, &sh->k_full[ks], 0, col * 128, h * C::DCH, b);
         ++kl;
-        if (sh->abort_flag || !mbar_wait(&sh->v_empty[vs], (uint32_t)((j >> 1) & 1) ^ 1, limit_ns)) { ok = false; break; }
+        if (sh->abort_flag || !mbar_await(&sh->v_empty[vs], (uint32_t)((j >> 1) & 1) ^ 1, limit_ns)) { ok = false; break; }
         mbar_arrive_expect_tx(&sh->v_full[vs], C::TILE);
-#pragma unroll
-        for (int ch = 0; ch < C::DCH; ++ch)
-          tma_load_3d(smem + C::DQ_OFF_V + vs * C::TILE + ch * 16384, &tm_v, &sh->v_full[vs], h * D + ch * 64, col * 128, b);
+        tma_load_4d(smem + C::DQ_OFF_V + vs * C::TILE, &tm_v, &sh->v_full[vs], 0, col * 128, h * C::DCH, b);
         ++vl;
       }
       if (!ok) diff_bwd_timeout(sh, status);
       // every copy this thread started lands before the CTA exits
-      mbar_wait(&sh->fixed_full, 0, kDiffBwdDrainNs);
+      mbar_await(&sh->fixed_full, 0, kDiffBwdDrainNs);
       for (int i = (kl > 3 ? kl - 3 : 0); i < kl; ++i)
-        mbar_wait(&sh->k_full[i % 3], (uint32_t)((i / 3) & 1), kDiffBwdDrainNs);
+        mbar_await(&sh->k_full[i % 3], (uint32_t)((i / 3) & 1), kDiffBwdDrainNs);
       for (int i = (vl > 2 ? vl - 2 : 0); i < vl; ++i)
-        mbar_wait(&sh->v_full[i & 1], (uint32_t)((i >> 1) & 1), kDiffBwdDrainNs);
+        mbar_await(&sh->v_full[i & 1], (uint32_t)((i >> 1) & 1), kDiffBwdDrainNs);
     }
-  } else if (warp == 0) {
-    // ---------------------------------------------------------- tcgen05 issuer
-    if (lane == 0 && n > 0) {
-      auto k_tile = [&](int j) { return sbase + C::DQ_OFF_K + (j % 3) * C::TILE; };
-      auto v_tile = [&](int j) { return sbase + C::DQ_OFF_V + (j & 1) * C::TILE; };
-      auto wait_k = [&](int j) { return mbar_wait(&sh->k_full[j % 3], (uint32_t)((j / 3) & 1), limit_ns); };
-      auto wait_v = [&](int j) { return mbar_wait(&sh->v_full[j & 1], (uint32_t)((j >> 1) & 1), limit_ns); };
-      auto issue_s = [&](int j) {
-        mma_steps<D / 32>(tmem + TM_S, q_s, k_tile(j), 0, C::IDESC_S);
-        mma_steps<D / 32>(tmem + TM_S + 128, q_s, k_tile(j), D / 32, C::IDESC_S);
-        mma_commit(&sh->s_full);
-      };
-      auto issue_dp = [&](int j) {
-        mma_steps<D / 16>(tmem + TM_DP, do_s, v_tile(j), 0, C::IDESC_S);
-        mma_commit(&sh->dp_full);
-        mma_commit(&sh->v_empty[j & 1]);
-      };
-      // S of the next tile as soon as the row warps hold S in registers; then the
-      // gradient products and, behind them in the issue order, dP of the next
-      // tile over dS.
-      bool ok = mbar_wait(&sh->fixed_full, 0, limit_ns) && wait_k(0) && wait_v(0);
-      if (ok) {
-        tc_fence_after();
-        issue_s(0);
-        issue_dp(0);
-      }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- tcgen05 issuer of S: of the
+    // next tile as soon as the row warps hold S in registers
+    if (n > 0) {  // (the whole warp; one lane issues)
+      bool ok = mbar_await_warp(&sh->fixed_full, 0, limit_ns);
+      int s = 0;
+      uint32_t ph = 0;  // K stage and its parity
       for (int j = 0; ok && j < n; ++j) {
-        if (j + 1 < n) {
-          if (sh->abort_flag || !wait_k(j + 1) || !mbar_wait(&sh->s_read, (uint32_t)(j & 1), limit_ns)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          issue_s(j + 1);
+        if (__any_sync(0xffffffffu, sh->abort_flag) || !mbar_await_warp(&sh->k_full[s], ph, limit_ns) ||
+            (j > 0 && !mbar_await_warp(&sh->s_read, (uint32_t)((j - 1) & 1), limit_ns))) {
+          ok = false;
+          break;
         }
-        if (sh->abort_flag || !mbar_wait(&sh->ds_full, (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
         tc_fence_after();
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ts(tmem + TM_DQ + 64 * m, tmem + TM_DP + 64 * (kk >> 2) + 32 * m + 8 * (kk & 3),
-                        sw128_desc(k_tile(j) + (C::DCH == 2 ? m * 16384 : 0) + kk * 2048, 16384, 1024), C::IDESC_H,
-                        (j > 0 || kk > 0) ? 1u : 0u);
-        mma_commit(&sh->k_empty[j % 3]);
-        if (j + 1 == n) mma_commit(&sh->mm_done);
-        if (j + 1 < n) {
-          if (!wait_v(j + 1)) { ok = false; break; }
-          tc_fence_after();
-          issue_dp(j + 1);
+        if (elect_one()) {
+          const uint32_t kt = sbase + C::DQ_OFF_K + s * C::TILE;
+          mma_steps<D / 32>(tmem + TM_S, q_s, kt, 0, C::IDESC_S);
+          mma_steps<D / 32>(tmem + TM_S + 128, q_s, kt, D / 32, C::IDESC_S);
+          mma_commit(&sh->s_full);
         }
+        s = s == 2 ? 0 : s + 1;
+        ph = s == 0 ? ph ^ 1 : ph;
       }
       if (!ok) diff_bwd_timeout(sh, status);
       // every product has ended before the tensor memory is given back, also when a row warp gave up
-      mma_commit(&sh->drain);
-      mbar_wait(&sh->drain, 0, kDiffBwdDrainNs);
+      if (elect_one()) mma_commit(&sh->drain);
+      mbar_await_warp(&sh->drain, 0, kDiffBwdDrainNs);
     }
-  } else if (warp >= 2) {
+  } else if (warp == 2) {
+    // ---------------------------------------------------------- tcgen05 issuer of dP and dQ:
+    // dP of the next tile over dS, behind the products that read it
+    if (n > 0) {
+      auto issue_dp = [&](int j) {
+        mma_steps<D / 16>(tmem + TM_DP, do_s, sbase + C::DQ_OFF_V + (j & 1) * C::TILE, 0, C::IDESC_S);
+        mma_commit(&sh->dp_full);
+        mma_commit(&sh->v_empty[j & 1]);
+      };
+      bool ok = mbar_await_warp(&sh->fixed_full, 0, limit_ns) && mbar_await_warp(&sh->v_full[0], 0, limit_ns);
+      if (ok) {
+        tc_fence_after();
+        if (elect_one()) issue_dp(0);
+      }
+      int s = 0;
+      uint32_t ph = 0;
+      for (int j = 0; ok && j < n; ++j) {
+        if (__any_sync(0xffffffffu, sh->abort_flag) || !mbar_await_warp(&sh->k_full[s], ph, limit_ns) ||
+            (j + 1 < n && !mbar_await_warp(&sh->v_full[(j + 1) & 1], (uint32_t)(((j + 1) >> 1) & 1), limit_ns)) ||
+            !mbar_await_warp(&sh->ds_full, (uint32_t)(j & 1), limit_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t kt = sbase + C::DQ_OFF_K + s * C::TILE;
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              mma_bf16_ts(tmem + TM_DQ + 64 * m, tmem + TM_DP + 64 * (kk >> 2) + 32 * m + 8 * (kk & 3),
+                          sw128_desc(kt + (C::DCH == 2 ? m * 16384 : 0) + kk * 2048, 16384, 1024), C::IDESC_H,
+                          (j > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&sh->k_empty[s]);  // (S of this tile ended before the row warps formed dS)
+          if (j + 1 < n)
+            issue_dp(j + 1);
+          else
+            mma_commit(&sh->mm_done);
+        }
+        s = s == 2 ? 0 : s + 1;
+        ph = s == 0 ? ph ^ 1 : ph;
+      }
+      if (!ok) diff_bwd_timeout(sh, status);
+      if (elect_one()) mma_commit(&sh->drain);
+      mbar_await_warp(&sh->drain, 0, kDiffBwdDrainNs);
+    }
+  } else if (warp >= 4) {
     // one thread a query row and half of the keys of every tile
-    const int quarter = warp & 3, r = quarter * 32 + lane, half = (warp - 2) >> 2;
+    const int quarter = warp & 3, r = quarter * 32 + lane, half = (warp - 4) >> 2;
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
-    const size_t total = (size_t)(gridDim.x / nb) * npad, at = (size_t)bh * npad + qt * 128 + r;
-    const float l1 = rows[at], l2 = rows[total + at], D1 = rows[2 * total + at], D2 = rows[3 * total + at];
+    const float* at = rows + ((size_t)bh * npad + qt * 128 + (r & 64)) * 4 + (r & 63);
+    const float l1 = at[0], l2 = at[64], D1 = at[128], D2 = at[192];
     const uint64_t c2 = f32x2_pack(scale_log2, scale_log2), nl1 = f32x2_pack(-l1, -l1), nl2 = f32x2_pack(-l2, -l2);
     const uint64_t nd1 = f32x2_pack(-D1, -D1), nd2 = f32x2_pack(-D2, -D2);
     uint64_t dl2 = 0;  // (0, 0)
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const int valid = N - col_idx[c0 + j] * 128 - 64 * half;  // real keys from this half's first on
-      if (!mbar_wait_warp(&sh->s_full, (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
+      if (!mbar_await_warp(&sh->s_full, (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
       tc_fence_after();
       // P_1, then P_2: S is released once both are in registers, so that S of the
       // next tile runs beside P_2's exponentials
@@ -351,7 +367,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       if (lane == 0) mbar_arrive(&sh->s_read);
 #pragma unroll
       for (int c = 0; c < 2; ++c) diff_exp32(p2[c], c2, nl2, valid - 32 * c);
-      if (!mbar_wait_warp(&sh->dp_full, (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
+      if (!mbar_await_warp(&sh->dp_full, (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
       tc_fence_after();
       // (both chunks of a thread's dP are read before dS takes their place: the
       // first chunk's dS_1 lies over the first chunk, its dS_2 over the second)
@@ -386,7 +402,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->ds_full);
     }
-    if (ok && n >= 1) ok = mbar_wait_warp(&sh->mm_done, 0, limit_ns);  // the last gradient products
+    if (ok && n >= 1) ok = mbar_await_warp(&sh->mm_done, 0, limit_ns);  // the last gradient products
     if (!ok) {
       diff_bwd_timeout(sh, status);
     } else {
@@ -412,7 +428,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     dl += dl_odd;
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) dl += __shfl_xor_sync(0xffffffffu, dl, o);
-    if (lane == 0) sh->part[warp - 2] = dl;
+    if (lane == 0) sh->part[warp - 4] = dl;
   }
   __syncwarp();
   tc_fence_before();
@@ -459,11 +475,11 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(&sh->fixed_full, 1);
     for (int s = 0; s < C::STAGES; ++s) mbar_init(&sh->ring_full[s], 1), mbar_init(&sh->ring_empty[s], 1);
-    mbar_init(&sh->s_full, 1);
+    mbar_init(&sh->s_full, 2);  // the scores and dP^T
     mbar_init(&sh->s_read, 8);
     mbar_init(&sh->ds_full, 8);
     mbar_init(&sh->mm_done, 1);
-    mbar_init(&sh->drain, 1);
+    mbar_init(&sh->drain, 3);
     sh->abort_flag = 0;
     fence_mbar_init();
   }
@@ -474,102 +490,92 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh->tmem_base;
+  constexpr uint32_t tmem = 0;  // all 512 columns are this CTA's: they begin at 0
   const uint32_t k_s = sbase + C::OFF_FIX, v_s = k_s + C::TILE;
 
-  if (warp == 1) {
+  if (warp == 0) {
     // ---------------------------------------------------------- TMA producer
     if (lane == 0) {
       bool ok = true;
       int loads = 0;
       mbar_arrive_expect_tx(&sh->fixed_full, 2 * C::TILE);
-#pragma unroll
-      for (int ch = 0; ch < C::DCH; ++ch) {
-        tma_load_3d(smem + C::OFF_FIX + ch * 16384, &tm_k, &sh->fixed_full, h * D + ch * 64, kt * 128, b);
-        tma_load_3d(smem + C::OFF_FIX + C::TILE + ch * 16384, &tm_v, &sh->fixed_full, h * D + ch * 64, kt * 128, b);
-      }
+      tma_load_4d(smem + C::OFF_FIX, &tm_k, &sh->fixed_full, 0, kt * 128, h * C::DCH, b);
+      tma_load_4d(smem + C::OFF_FIX + C::TILE, &tm_v, &sh->fixed_full, 0, kt * 128, h * C::DCH, b);
       // step i: rows [64 (i & 1), + 64) of query tile i / 2, into the stage that
       // the gradient products of step i - 4 have read
       int qi = 0;
       for (int i = 0; i < 2 * n; ++i) {
         if ((i & 1) == 0) qi = t_col_idx[c0 + (i >> 1)];
         const int s = i % C::STAGES, q0 = qi * 128 + 64 * (i & 1);
-        if (sh->abort_flag || !mbar_wait(&sh->ring_empty[s], (uint32_t)((i / C::STAGES) & 1) ^ 1, limit_ns)) {
+        if (sh->abort_flag || !mbar_await(&sh->ring_empty[s], (uint32_t)((i / C::STAGES) & 1) ^ 1, limit_ns)) {
           ok = false;
           break;
         }
         uint8_t* dst = smem + C::OFF_RING + s * 2 * C::HALF;
         float* vec = reinterpret_cast<float*>(smem + C::OFF_VEC + s * C::VEC);
         mbar_arrive_expect_tx(&sh->ring_full[s], 2 * C::HALF + C::VEC);
-#pragma unroll
-        for (int ch = 0; ch < C::DCH; ++ch) {
-          tma_load_3d(dst + ch * 8192, &tm_q, &sh->ring_full[s], h * D + ch * 64, q0, b);
-          tma_load_3d(dst + C::HALF + ch * 8192, &tm_do, &sh->ring_full[s], h * D + ch * 64, q0, b);
-        }
-        const size_t total = (size_t)(gridDim.x / nb) * npad, at = (size_t)bh * npad + (size_t)q0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) bulk_load(vec + 64 * x, rows + x * total + at, 256, &sh->ring_full[s]);
+        tma_load_4d(dst, &tm_q, &sh->ring_full[s], 0, q0, h * C::DCH, b);
+        tma_load_4d(dst + C::HALF, &tm_do, &sh->ring_full[s], 0, q0, h * C::DCH, b);
+        bulk_load(vec, rows + ((size_t)bh * npad + (size_t)q0) * 4, C::VEC, &sh->ring_full[s]);
         ++loads;
       }
       if (!ok) diff_bwd_timeout(sh, status);
       // every copy this thread started lands before the CTA exits
-      mbar_wait(&sh->fixed_full, 0, kDiffBwdDrainNs);
+      mbar_await(&sh->fixed_full, 0, kDiffBwdDrainNs);
       for (int i = (loads > C::STAGES ? loads - C::STAGES : 0); i < loads; ++i)
-        mbar_wait(&sh->ring_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), kDiffBwdDrainNs);
+        mbar_await(&sh->ring_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), kDiffBwdDrainNs);
     }
-  } else if (warp == 0) {
-    // ---------------------------------------------------------- tcgen05 issuer
-    if (lane == 0 && n > 0) {
-      auto stage = [&](int i) { return sbase + C::OFF_RING + (i % C::STAGES) * 2 * C::HALF; };
-      auto wait_q = [&](int i) {
-        return mbar_wait(&sh->ring_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), limit_ns);
-      };
-      auto issue_s = [&](int i) {
-        const uint32_t qs = stage(i);
-        mma_steps<D / 32>(tmem + TM_S, k_s, qs, 0, C::IDESC_SH, 8192);
-        mma_steps<D / 32>(tmem + TM_S + 64, k_s, qs, D / 32, C::IDESC_SH, 8192);
-        mma_steps<D / 16>(tmem + TM_DP, v_s, qs + C::HALF, 0, C::IDESC_SH, 8192);
-        mma_commit(&sh->s_full);
-      };
-      const int steps = 2 * n;
-      bool ok = mbar_wait(&sh->fixed_full, 0, limit_ns) && wait_q(0);
-      if (ok) {
+  } else if (warp < 4) {
+    // ---------------------------------------------------------- tcgen05 issuers: S^T of both
+    // maps (warp 1) and dP^T (warp 2) of a step as soon as the row warps hold the
+    // ones before in registers, the gradient products (warp 3) once their operands
+    // are written
+    if (n > 0) {  // (whole warps; one lane issues)
+      bool ok = mbar_await_warp(&sh->fixed_full, 0, limit_ns);
+      for (int i = 0; ok && i < 2 * n; ++i) {
+        const int s = i % C::STAGES;
+        const uint32_t qs = sbase + C::OFF_RING + s * 2 * C::HALF;
+        if (__any_sync(0xffffffffu, sh->abort_flag) ||
+            !mbar_await_warp(&sh->ring_full[s], (uint32_t)((i / C::STAGES) & 1), limit_ns) ||
+            (warp < 3 && i > 0 && !mbar_await_warp(&sh->s_read, (uint32_t)((i - 1) & 1), limit_ns)) ||
+            (warp == 3 && !mbar_await_warp(&sh->ds_full, (uint32_t)(i & 1), limit_ns))) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        issue_s(0);
-      }
-      // Step i: the next scores as soon as this step's are in the row warps'
-      // registers, then this step's gradient products once their operands are written.
-      for (int i = 0; ok && i < steps; ++i) {
-        if (i + 1 < steps) {
-          if (sh->abort_flag || !wait_q(i + 1) || !mbar_wait(&sh->s_read, (uint32_t)(i & 1), limit_ns)) {
-            ok = false;
-            break;
+        if (warp == 1) {
+          if (elect_one()) {
+            mma_steps<D / 32>(tmem + TM_S, k_s, qs, 0, C::IDESC_SH, 8192);
+            mma_steps<D / 32>(tmem + TM_S + 64, k_s, qs, D / 32, C::IDESC_SH, 8192);
+            mma_commit(&sh->s_full);
           }
-          tc_fence_after();
-          issue_s(i + 1);
-        }
-        if (sh->abort_flag || !mbar_wait(&sh->ds_full, (uint32_t)(i & 1), limit_ns)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t qs = stage(i), ds_s = sbase + C::OFF_DS;
+        } else if (warp == 2) {
+          if (elect_one()) {
+            mma_steps<D / 16>(tmem + TM_DP, v_s, qs + C::HALF, 0, C::IDESC_SH, 8192);
+            mma_commit(&sh->s_full);
+          }
+        } else if (elect_one()) {
+          const uint32_t ds_s = sbase + C::OFF_DS;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const uint32_t acc = (i > 0 || kk > 0) ? 1u : 0u;
-          mma_bf16_ts(tmem + TM_DV, tmem + TM_A + 8 * kk, sw128_desc(qs + C::HALF + kk * 2048, 8192, 1024), C::IDESC_V, acc);
-          mma_bf16_ts(tmem + TM_DK, tmem + TM_DS + 8 * kk, sw128_desc(qs + kk * 2048, 8192, 1024), C::IDESC_H, acc);
-          mma_bf16_ss(tmem + TM_DK + 64, sw128_desc(ds_s + kk * 32, 16, 1024),
-                      sw128_desc(qs + (C::DCH == 2 ? 8192 : 0) + kk * 2048, 8192, 1024), C::IDESC_H, acc);
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t acc = (i > 0 || kk > 0) ? 1u : 0u;
+            mma_bf16_ts(tmem + TM_DV, tmem + TM_A + 8 * kk, sw128_desc(qs + C::HALF + kk * 2048, 8192, 1024), C::IDESC_V, acc);
+            mma_bf16_ts(tmem + TM_DK, tmem + TM_DS + 8 * kk, sw128_desc(qs + kk * 2048, 8192, 1024), C::IDESC_H, acc);
+            mma_bf16_ss(tmem + TM_DK + 64, sw128_desc(ds_s + kk * 32, 16, 1024),
+                        sw128_desc(qs + (C::DCH == 2 ? 8192 : 0) + kk * 2048, 8192, 1024), C::IDESC_H, acc);
+          }
+          mma_commit(&sh->mm_done);
+          mma_commit(&sh->ring_empty[s]);
         }
-        mma_commit(&sh->mm_done);
-        mma_commit(&sh->ring_empty[i % C::STAGES]);
       }
       if (!ok) diff_bwd_timeout(sh, status);
       // every product has ended before the tensor memory is given back, also when a row warp gave up
-      mma_commit(&sh->drain);
-      mbar_wait(&sh->drain, 0, kDiffBwdDrainNs);
+      if (elect_one()) mma_commit(&sh->drain);
+      mbar_await_warp(&sh->drain, 0, kDiffBwdDrainNs);
     }
-  } else if (warp >= 2) {
+  } else {
     // one thread a key row and half of a step's queries
-    const int quarter = warp & 3, r = quarter * 32 + lane, half = (warp - 2) >> 2;
+    const int quarter = warp & 3, r = quarter * 32 + lane, half = (warp - 4) >> 2;
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
     const float lh = diff_lambda(lam, lam_bf16, h);
     const uint64_t c2 = f32x2_pack(scale_log2, scale_log2), nlam = f32x2_pack(-lh, -lh);
@@ -577,8 +583,8 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     bool ok = true;
     for (int i = 0; i < 2 * n; ++i) {
       const int s = i % C::STAGES;
-      if (!mbar_wait_warp(&sh->s_full, (uint32_t)(i & 1), limit_ns) ||
-          !mbar_wait_warp(&sh->ring_full[s], (uint32_t)((i / C::STAGES) & 1), limit_ns)) {
+      if (!mbar_await_warp(&sh->s_full, (uint32_t)(i & 1), limit_ns) ||
+          !mbar_await_warp(&sh->ring_full[s], (uint32_t)((i / C::STAGES) & 1), limit_ns)) {
         ok = false;
         break;
       }
@@ -623,7 +629,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
         }
       }
       // the products of the step before have read the operands' places
-      if (i >= 1 && !mbar_wait_warp(&sh->mm_done, (uint32_t)((i - 1) & 1), limit_ns)) { ok = false; break; }
+      if (i >= 1 && !mbar_await_warp(&sh->mm_done, (uint32_t)((i - 1) & 1), limit_ns)) { ok = false; break; }
       tc_fence_after();
       tmem_st16(lane_addr + TM_A + 16 * half, a);
       tmem_st16(lane_addr + TM_DS + 16 * half, z1);
@@ -637,7 +643,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->ds_full);
     }
-    if (ok && n >= 1) ok = mbar_wait_warp(&sh->mm_done, (uint32_t)((2 * n - 1) & 1), limit_ns);
+    if (ok && n >= 1) ok = mbar_await_warp(&sh->mm_done, (uint32_t)((2 * n - 1) & 1), limit_ns);
     if (!ok) {
       diff_bwd_timeout(sh, status);
     } else {

@@ -227,7 +227,7 @@ cudaError_t launch_narrow3(const float* x, uint16_t* y0, uint16_t* y1, uint16_t*
 
 // Differential attention (diff.cu, diff_bwd.cu, diff_decode.cu); raster blocks of 128 tokens.
 struct DiffArgs {
-  const CUtensorMap *tm_q, *tm_k, *tm_v;  // box (64, 128, 1)
+  const CUtensorMap *tm_q, *tm_k, *tm_v;  // box (64, 128, d/64, 1)
   const CUtensorMap *tm_out, *tm_out2;    // forward (tm_out2: with lse)
   const CUtensorMap *tm_do, *tm_q64, *tm_do64;  // backward (boxes of 128 and of 64 rows)
   const int32_t *row_ptr, *col_idx, *t_row_ptr, *t_col_idx;
@@ -237,7 +237,7 @@ struct DiffArgs {
   const uint16_t *out, *out2, *dout;      // backward
   uint16_t *dq, *dk, *dv;
   void* dlam;
-  float* rows;                            // workspace: [4][B*Hh][npad]
+  float* rows;                            // workspace: [B*Hh][npad/64][4][64]
   float* dlam_part;                       // workspace: [B*Hh][nb]
   int B, N, heads, d, nb, npad, mask_per_bh;
   float scale, scale_log2;

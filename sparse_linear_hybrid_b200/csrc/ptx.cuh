@@ -74,6 +74,25 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, u
   return __all_sync(0xffffffffu, ok);
 }
 
+// mbar_wait and mbar_wait_warp that only look when the limit is 0: try_wait may
+// suspend the thread for a while and find the phase complete after all.
+__device__ __forceinline__ bool mbar_await(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  if (limit_ns != 0) return mbar_wait(bar, parity, limit_ns);
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_await_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  const bool ok = mbar_await(bar, parity, limit_ns);
+  return __all_sync(0xffffffffu, ok);
+}
+
 // ---------------------------------------------------------------- fences
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -138,6 +157,17 @@ __device__ __forceinline__ void bulk_wait_group_read0() {
 }
 
 // ---------------------------------------------------------------- tcgen05
+// True in one lane of a converged warp, always the same one.  An issuing warp
+// that runs its loop as a whole and branches on this only around the products
+// keeps their descriptors in uniform registers; a single thread that runs the
+// loop (lane == 0) moves them there for every product: 128 x 64 x 16 products
+// from tensor memory issue every 33 cycles this way and every 55 the other,
+// 16 alternating ones from shared and tensor memory in 1,040 against 1,980.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
                "r"(ncols)
