@@ -7,18 +7,16 @@
 // tiles; both maps read the same K and V tiles.
 //
 // Tensor memory (512 columns): S_1 [0,128), S_2 [128,256), O_1 [256,256+d),
-// O_2 [384,384+d); P_m as bf16 over the last 64 columns of S_m, so S_m of the
+// O_2 [384,384+d); P_m as bf16 over the first 64 columns of S_m, so S_m of the
 // next tile follows P_m V in the issue order.  The maps alternate: while the four
 // softmax warps of map 1 work, the tensor cores run P_2 V and S_2 of the next
 // tile, and the other way round.
 // Warp roles, 384 threads: warp 0 TMA producer (K and V rings of three tiles),
 // warp 1 tcgen05 issuer and owner of the tensor memory, warps 4-7 softmax of map
-// 1 and warps 8-11 of map 2, one thread a query row.  Map 2's warps begin after
-// map 1's have written their first P: the two groups then stay half a tile apart,
-// one in the exponentials while the other waits for its products.  The running maximum only
-// moves (and O_m is rescaled in tensor memory) when it grows by more than 2^8.
-// The row sum adds the bf16-rounded p that the value product reads, so the
-// rounding of a dominant key cancels in O / l.  At the end the two warp groups
+// 1 and warps 8-11 of map 2, one thread a query row.  P enters its
+// product as bf16 (2^-9 of each weight, a fifth of the output's own rounding in a
+// row of many keys); the row sum and the log-sum-exp add the unrounded p.
+// At the end the two warp groups
 // exchange the row sums and each writes half of the features of its row.
 //
 // Bound by the exponentials: 2 x 128 x 128 a tile pair, 16 a clock and SM on the
@@ -33,7 +31,7 @@ namespace {
 
 constexpr int kDiffThreads = 384;
 constexpr uint64_t kDiffDrainNs = 1000000000ull;
-constexpr float kDiffRescale = 8.0f;  // log2 units
+constexpr float kDiffGrown = 1.152921504606847e18f;  // 2^60
 constexpr float kLn2 = 0.69314718055994531f;
 
 struct DiffShared {
@@ -42,7 +40,6 @@ struct DiffShared {
   uint64_t s_full[2];   // per map: S of the current tile is in tensor memory (and the P V before it is done)
   uint64_t p_full[2];   // per map: the four softmax warps have written P
   uint64_t o_full;      // every product is done
-  uint64_t turn;        // map 1's softmax warps have written their first P
   uint64_t drain;
   uint32_t tmem_base;
   volatile int abort_flag;
@@ -77,12 +74,71 @@ __device__ __forceinline__ float lambda_of(const void* lam, int bf16, int h) {
 }
 
 // -inf in place of the scores from column `valid` on.
-__device__ __forceinline__ void mask_keys(uint32_t (&sr)[64], int valid) {
-  if (valid < 64) {
+__device__ __forceinline__ void mask_keys(uint32_t (&sr)[32], int valid) {
+  if (valid < 32) {
 #pragma unroll
-    for (int i = 0; i < 64; ++i)
+    for (int i = 0; i < 32; ++i)
       if (i >= valid) sr[i] = __float_as_uint(-INFINITY);
   }
+}
+
+__device__ __forceinline__ void max_of(const uint32_t (&sr)[32], float (&m)[4]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      m[k] = fmax3(m[k], __uint_as_float(sr[i + 2 * k]), __uint_as_float(sr[i + 2 * k + 1]));
+}
+
+// The maximum of 64 scores of the row.
+__device__ __forceinline__ float row_max(uint32_t s_addr, int valid) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  uint32_t sr[2][32];
+  tmem_ld32(s_addr, sr[0]);
+  tmem_ld32(s_addr + 32, sr[1]);
+  tmem_ld_wait();
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    mask_keys(sr[c], valid - 32 * c);
+    max_of(sr[c], m);
+  }
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// p = 2^(s c + b) of 64 scores of the row as bf16 pairs; returns their sum.
+__device__ __forceinline__ float softmax_pass(uint32_t s_addr, int valid, uint64_t c2, float b, uint32_t (&pk)[32]) {
+  const uint64_t b2 = f32x2_pack(b, b);
+  uint64_t acc0 = 0, acc1 = 0;
+  uint32_t sr[2][32];
+  tmem_ld32(s_addr, sr[0]);
+  tmem_ld32(s_addr + 32, sr[1]);
+  tmem_ld_wait();
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t(&x)[32] = sr[c];
+    mask_keys(x, valid - 32 * c);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint64_t e = f32x2_fma(f32x2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, b2);
+      float p0, p1;
+      if ((i & 3) == 3) {
+        exp2_fma_x2(e, p0, p1);
+      } else {
+        float x0, x1;
+        f32x2_unpack(e, x0, x1);
+        p0 = ex2_approx(x0);
+        p1 = ex2_approx(x1);
+      }
+      pk[16 * c + i] = pack_bf16x2(p0, p1);
+      if (i & 1)
+        acc1 = f32x2_add(acc1, f32x2_pack(p0, p1));
+      else
+        acc0 = f32x2_add(acc0, f32x2_pack(p0, p1));
+    }
+  }
+  float a0, a1;
+  f32x2_unpack(f32x2_add(acc0, acc1), a0, a1);
+  return a0 + a1;
 }
 
 // TRAIN: also O_2 / l_2 and the log-sum-exps of both maps.
@@ -119,7 +175,6 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       mbar_init(&sh->p_full[m], 4);
     }
     mbar_init(&sh->o_full, 1);
-    mbar_init(&sh->turn, 4);
     mbar_init(&sh->drain, 1);
     sh->abort_flag = 0;
     fence_mbar_init();
@@ -201,7 +256,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
             const uint32_t vt = sbase + C::OFF_V + s * C::TILE;
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              mma_bf16_ts(tmem + C::TM_O + 128 * m, tmem + C::TM_S + 128 * m + 64 + kk * 8,
+              mma_bf16_ts(tmem + C::TM_O + 128 * m, tmem + C::TM_S + 128 * m + kk * 8,
                           sw128_desc(vt + kk * 2048, 16384, 1024), C::IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
             if (m == 1) mma_commit(&sh->v_empty[s]);
             if (j + 1 < n) issue_s(m, s1);  // over P, behind the product that reads it
@@ -225,110 +280,66 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t s_addr = lane_addr + C::TM_S + 128 * m, o_addr = lane_addr + C::TM_O + 128 * m;
     const uint64_t c2 = f32x2_pack(scale_log2, scale_log2);
-    float m_ref = -INFINITY, l = 0.f, le = 0.f;
+    float m_ref = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       const int valid = N - col_idx[c0 + j] * 128;  // real keys of the tile
-      if (!mbar_await_warp(&sh->s_full[m], (uint32_t)(j & 1), limit_ns) ||
-          (m == 1 && j == 0 && !mbar_await_warp(&sh->turn, 0, limit_ns))) {
-        ok = false;
-        break;
-      }
+      if (!mbar_await_warp(&sh->s_full[m], (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
       tc_fence_after();
-      // The row's maximum.  The second half of the scores stays in registers, the
-      // first is read again below: all 128 at once would not leave enough for the rest.
-      uint32_t sr[64];
-      float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+      // The reference is the first tile's maximum, and later tiles' exponentials
+      // are taken against it without looking for their own: fp32 and bf16 hold p
+      // and its sums up to far above 2^60, and a row's precision does not depend
+      // on their common factor.  Only when 64 keys' sum passes 2^60 does the row
+      // take their maximum as its new reference, with O, l and the first keys' P
+      // scaled down and the exponentials taken again (the scores are still there).
+      if (j == 0) m_ref = fmaxf(row_max(s_addr, valid), row_max(s_addr + 64, valid - 64));
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        tmem_ld32(s_addr + 64 * hf, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-        tmem_ld32(s_addr + 64 * hf + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-        tmem_ld_wait();
-        mask_keys(sr, valid - 64 * hf);
-#pragma unroll
-        for (int i = 0; i < 64; i += 8) {
-          m0 = fmax3(m0, __uint_as_float(sr[i + 0]), __uint_as_float(sr[i + 1]));
-          m1 = fmax3(m1, __uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3]));
-          m2 = fmax3(m2, __uint_as_float(sr[i + 4]), __uint_as_float(sr[i + 5]));
-          m3 = fmax3(m3, __uint_as_float(sr[i + 6]), __uint_as_float(sr[i + 7]));
-        }
-      }
-      const float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
-      float alpha = 1.f;
-      bool rescale = false;
-      if (m_ref == -INFINITY) {
-        m_ref = mt;
-      } else if ((mt - m_ref) * scale_log2 > kDiffRescale) {
-        alpha = ex2_approx((m_ref - mt) * scale_log2);
-        m_ref = mt;
-        rescale = true;
-      }
-      if (__any_sync(0xffffffffu, rescale)) {
-        // (the product that wrote O last came before S of this tile)
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t rr[32];
-          tmem_ld32(o_addr + 32 * c, rr);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) rr[i] = __float_as_uint(__uint_as_float(rr[i]) * alpha);
-          tmem_st32(o_addr + 32 * c, rr);
-        }
-      }
-      const uint64_t nmb2 = f32x2_pack(-m_ref * scale_log2, -m_ref * scale_log2);
-      uint64_t acc0 = 0, acc1 = 0, acce = 0;
-#pragma unroll
-      for (int hf = 1; hf >= 0; --hf) {
-        if (hf == 0) {
-          tmem_ld32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-          tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-          tmem_ld_wait();
-          mask_keys(sr, valid);
-        }
         uint32_t pk[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const uint64_t x = f32x2_fma(f32x2_pack(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), c2, nmb2);
-          float p0, p1;
-          if ((i & 3) == 3) {
-            exp2_fma_x2(x, p0, p1);
-          } else {
-            float x0, x1;
-            f32x2_unpack(x, x0, x1);
-            p0 = ex2_approx(x0);
-            p1 = ex2_approx(x1);
+        float rs = softmax_pass(s_addr + 64 * hf, valid - 64 * hf, c2, -m_ref * scale_log2, pk);
+        const bool grown = rs > kDiffGrown;
+        if (__any_sync(0xffffffffu, grown)) {
+          const float mt = row_max(s_addr + 64 * hf, valid - 64 * hf);
+          float alpha = 1.f;
+          if (grown) {
+            alpha = ex2_approx((m_ref - mt) * scale_log2);
+            m_ref = mt;
           }
-          pk[i] = pack_bf16x2(p0, p1);
-          if (TRAIN) acce = f32x2_add(acce, f32x2_pack(p0, p1));
-          const uint64_t pp = f32x2_pack(bf16_lo_to_f32(pk[i]), bf16_hi_to_f32(pk[i]));
-          if (i & 1)
-            acc1 = f32x2_add(acc1, pp);
-          else
-            acc0 = f32x2_add(acc0, pp);
+          l *= alpha;
+          if (j > 0) {  // (the product that wrote O last came before S of this tile)
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              tmem_ld32(o_addr + 32 * c, pk);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) pk[i] = __float_as_uint(__uint_as_float(pk[i]) * alpha);
+              tmem_st32(o_addr + 32 * c, pk);
+            }
+          }
+          if (hf == 1) {
+            tmem_ld32(s_addr, pk);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              pk[i] = pack_bf16x2(bf16_lo_to_f32(pk[i]) * alpha, bf16_hi_to_f32(pk[i]) * alpha);
+            tmem_st32(s_addr, pk);
+          }
+          rs = softmax_pass(s_addr + 64 * hf, valid - 64 * hf, c2, -m_ref * scale_log2, pk);
         }
-        tmem_st32(s_addr + 64 + 32 * hf, pk);
+        l += rs;
+        tmem_st32(s_addr + 32 * hf, pk);  // over scores that have been read
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sh->p_full[m]);
-        if (m == 0 && j == 0) mbar_arrive(&sh->turn);
-      }
-      float a0, a1;
-      f32x2_unpack(f32x2_add(acc0, acc1), a0, a1);
-      l = l * alpha + (a0 + a1);
-      if (TRAIN) {
-        f32x2_unpack(acce, a0, a1);
-        le = le * alpha + (a0 + a1);
-      }
+      if (lane == 0) mbar_arrive(&sh->p_full[m]);
     }
     if (ok && n > 0) ok = mbar_await_warp(&sh->o_full, 0, limit_ns);
     if (!ok) diff_timeout(sh, status);
     const int row = qt * 128 + r;
     if (TRAIN && ok && row < N) {
       const size_t BH = gridDim.x / nb;
-      lse[((size_t)m * BH + bh) * N + row] = n > 0 ? (m_ref * scale_log2 + log2f(le)) * kLn2 : -INFINITY;
+      lse[((size_t)m * BH + bh) * N + row] = n > 0 ? (m_ref * scale_log2 + log2f(l)) * kLn2 : -INFINITY;
     }
     sh->sum[m][r] = l;
     named_bar_sync(1, 256);  // (reached by every softmax thread, after a time-out too)
