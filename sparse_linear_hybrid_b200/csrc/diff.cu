@@ -199,22 +199,22 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       for (int j = 0; j < n; ++j) {
         const int s = j % C::STAGES, col = col_idx[c0 + j];
         const uint32_t ph = (uint32_t)((j / C::STAGES) & 1);
-        if (sh->abort_flag || !mbar_await(&sh->k_empty[s], ph ^ 1, limit_ns)) { ok = false; break; }
+        if (!mbar_wait(&sh->k_empty[s], ph ^ 1, limit_ns)) { ok = false; break; }
         mbar_arrive_expect_tx(&sh->k_full[s], C::TILE);
         tma_load_4d(smem + C::OFF_K + s * C::TILE, &tm_k, &sh->k_full[s], 0, col * 128, h * C::DCH, b);
         ++kl;
-        if (sh->abort_flag || !mbar_await(&sh->v_empty[s], ph ^ 1, limit_ns)) { ok = false; break; }
+        if (!mbar_wait(&sh->v_empty[s], ph ^ 1, limit_ns)) { ok = false; break; }
         mbar_arrive_expect_tx(&sh->v_full[s], C::TILE);
         tma_load_4d(smem + C::OFF_V + s * C::TILE, &tm_v, &sh->v_full[s], 0, col * 128, h * C::DCH, b);
         ++vl;
       }
       if (!ok) diff_timeout(sh, status);
       // every copy this thread started lands before the CTA exits
-      mbar_await(&sh->q_full, 0, kDiffDrainNs);
+      mbar_wait(&sh->q_full, 0, kDiffDrainNs);
       for (int i = (kl > C::STAGES ? kl - C::STAGES : 0); i < kl; ++i)
-        mbar_await(&sh->k_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), kDiffDrainNs);
+        mbar_wait(&sh->k_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), kDiffDrainNs);
       for (int i = (vl > C::STAGES ? vl - C::STAGES : 0); i < vl; ++i)
-        mbar_await(&sh->v_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), kDiffDrainNs);
+        mbar_wait(&sh->v_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), kDiffDrainNs);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- tcgen05 issuer
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
         mma_commit(&sh->s_full[m]);
         if (m == 1) mma_commit(&sh->k_empty[s]);
       };
-      bool ok = mbar_await_warp(&sh->q_full, 0, limit_ns) && mbar_await_warp(&sh->k_full[0], 0, limit_ns);
+      bool ok = mbar_await(&sh->q_full, 0, limit_ns) && mbar_await(&sh->k_full[0], 0, limit_ns);
       if (ok) {
         tc_fence_after();
         if (elect_one()) {
@@ -245,11 +245,11 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       for (int j = 0; ok && j < n; ++j) {
         const int s1 = s + 1 == C::STAGES ? 0 : s + 1;
         const uint32_t ph1 = s1 == 0 ? ph ^ 1 : ph;
-        ok = mbar_await_warp(&sh->v_full[s], ph, limit_ns) &&
-             (j + 1 == n || mbar_await_warp(&sh->k_full[s1], ph1, limit_ns));
+        ok = mbar_await(&sh->v_full[s], ph, limit_ns) &&
+             (j + 1 == n || mbar_await(&sh->k_full[s1], ph1, limit_ns));
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          ok = ok && !__any_sync(0xffffffffu, sh->abort_flag) && mbar_await_warp(&sh->p_full[m], (uint32_t)(j & 1), limit_ns);
+          ok = ok && mbar_await(&sh->p_full[m], (uint32_t)(j & 1), limit_ns);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       }
       // every product has ended before the tensor memory is given back, also when a softmax warp gave up
       if (elect_one()) mma_commit(&sh->drain);
-      mbar_await_warp(&sh->drain, 0, kDiffDrainNs);
+      mbar_wait_warp(&sh->drain, 0, kDiffDrainNs);
     }
   } else if (warp >= 4) {
     const int m = (warp - 4) >> 2;  // the map
@@ -281,10 +281,11 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     const uint32_t s_addr = lane_addr + C::TM_S + 128 * m, o_addr = lane_addr + C::TM_O + 128 * m;
     const uint64_t c2 = f32x2_pack(scale_log2, scale_log2);
     float m_ref = -INFINITY, l = 0.f;
+    const int last = n > 0 ? N - col_idx[c0 + n - 1] * 128 : 0;  // (columns ascend: only the last tile can be short)
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      const int valid = N - col_idx[c0 + j] * 128;  // real keys of the tile
-      if (!mbar_await_warp(&sh->s_full[m], (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
+      const int valid = j + 1 == n ? last : 128;  // real keys of the tile
+      if (!mbar_await(&sh->s_full[m], (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
       tc_fence_after();
       // The reference is the first tile's maximum, and later tiles' exponentials
       // are taken against it without looking for their own: fp32 and bf16 hold p
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->p_full[m]);
     }
-    if (ok && n > 0) ok = mbar_await_warp(&sh->o_full, 0, limit_ns);
+    if (ok && n > 0) ok = mbar_await(&sh->o_full, 0, limit_ns);
     if (!ok) diff_timeout(sh, status);
     const int row = qt * 128 + r;
     if (TRAIN && ok && row < N) {
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     // features [m D/2, m D/2 + D/2) of this row: out = O_1 / l_1 - lam O_2 / l_2
     const float lh = lambda_of(lam, lam_bf16, h);
     const float i1 = n > 0 ? 1.f / sh->sum[0][r] : 0.f, i2 = n > 0 ? 1.f / sh->sum[1][r] : 0.f;
-    if (n == 0) mbar_await_warp(&sh->q_full, 0, limit_ns);  // the Q buffer is written over: its load must have landed
+    if (n == 0) mbar_await(&sh->q_full, 0, limit_ns);  // the Q buffer is written over: its load must have landed
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       const int f0 = m * (D / 2) + 32 * c;  // 32 features

@@ -46,7 +46,6 @@ struct DiffBwdShared {
   uint64_t s_full, dp_full, s_read, ds_full, mm_done;
   uint64_t drain;
   uint32_t tmem_base;
-  volatile int abort_flag;
   float part[8];  // dlam by warp
 };
 
@@ -78,10 +77,7 @@ struct DiffBwdCfg {
   static_assert(DQ_SMEM <= 232448 && SMEM <= 232448, "shared memory budget");
 };
 
-__device__ __forceinline__ void diff_bwd_timeout(DiffBwdShared* sh, uint32_t* status) {
-  sh->abort_flag = 1;
-  atomicOr(status, kStatusTimeout);
-}
+__device__ __forceinline__ void diff_bwd_timeout(uint32_t* status) { atomicOr(status, kStatusTimeout); }
 __device__ __forceinline__ float diff_lambda(const void* lam, int bf16, int h) {
   return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(lam)[h] << 16) : static_cast<const float*>(lam)[h];
 }
@@ -222,7 +218,6 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     mbar_init(&sh->ds_full, 8);
     mbar_init(&sh->mm_done, 1);
     mbar_init(&sh->drain, 2);
-    sh->abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -246,36 +241,34 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       // K_j is free once the gradient products of tile j have read it, V_j once dP_j is done
       for (int j = 0; j < n; ++j) {
         const int col = col_idx[c0 + j], ks = j % 3, vs = j & 1;
-        if (sh->abort_flag || !mbar_await(&sh->k_empty[ks], (uint32_t)((j / 3) & 1) ^ 1, limit_ns)) { ok = false; break; }
+        if (!mbar_wait(&sh->k_empty[ks], (uint32_t)((j / 3) & 1) ^ 1, limit_ns)) { ok = false; break; }
         mbar_arrive_expect_tx(&sh->k_full[ks], C::TILE);
         tma_load_4d(smem + C::DQ_OFF_K + ks * C::TILE, &tm_k, &sh->k_full[ks], 0, col * 128, h * C::DCH, b);
         ++kl;
-        if (sh->abort_flag || !mbar_await(&sh->v_empty[vs], (uint32_t)((j >> 1) & 1) ^ 1, limit_ns)) { ok = false; break; }
+        if (!mbar_wait(&sh->v_empty[vs], (uint32_t)((j >> 1) & 1) ^ 1, limit_ns)) { ok = false; break; }
         mbar_arrive_expect_tx(&sh->v_full[vs], C::TILE);
         tma_load_4d(smem + C::DQ_OFF_V + vs * C::TILE, &tm_v, &sh->v_full[vs], 0, col * 128, h * C::DCH, b);
         ++vl;
       }
-      if (!ok) diff_bwd_timeout(sh, status);
+      if (!ok) diff_bwd_timeout(status);
       // every copy this thread started lands before the CTA exits
-      mbar_await(&sh->fixed_full, 0, kDiffBwdDrainNs);
+      mbar_wait(&sh->fixed_full, 0, kDiffBwdDrainNs);
       for (int i = (kl > 3 ? kl - 3 : 0); i < kl; ++i)
-        mbar_await(&sh->k_full[i % 3], (uint32_t)((i / 3) & 1), kDiffBwdDrainNs);
+        mbar_wait(&sh->k_full[i % 3], (uint32_t)((i / 3) & 1), kDiffBwdDrainNs);
       for (int i = (vl > 2 ? vl - 2 : 0); i < vl; ++i)
-        mbar_await(&sh->v_full[i & 1], (uint32_t)((i >> 1) & 1), kDiffBwdDrainNs);
+        mbar_wait(&sh->v_full[i & 1], (uint32_t)((i >> 1) & 1), kDiffBwdDrainNs);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- tcgen05 issuer of S: of the
     // next tile as soon as the row warps hold S in registers
     if (n > 0) {  // (the whole warp; one lane issues)
-      bool ok = mbar_await_warp(&sh->fixed_full, 0, limit_ns);
+      bool ok = mbar_await(&sh->fixed_full, 0, limit_ns);
       int s = 0;
       uint32_t ph = 0;  // K stage and its parity
       for (int j = 0; ok && j < n; ++j) {
-        if (__any_sync(0xffffffffu, sh->abort_flag) || !mbar_await_warp(&sh->k_full[s], ph, limit_ns) ||
-            (j > 0 && !mbar_await_warp(&sh->s_read, (uint32_t)((j - 1) & 1), limit_ns))) {
-          ok = false;
-          break;
-        }
+        ok = ok && mbar_await(&sh->k_full[s], ph, limit_ns);
+        ok = ok && (j == 0 || mbar_await(&sh->s_read, (uint32_t)((j - 1) & 1), limit_ns));
+        if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
           const uint32_t kt = sbase + C::DQ_OFF_K + s * C::TILE;
@@ -286,10 +279,10 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
         s = s == 2 ? 0 : s + 1;
         ph = s == 0 ? ph ^ 1 : ph;
       }
-      if (!ok) diff_bwd_timeout(sh, status);
+      if (!ok) diff_bwd_timeout(status);
       // every product has ended before the tensor memory is given back, also when a row warp gave up
       if (elect_one()) mma_commit(&sh->drain);
-      mbar_await_warp(&sh->drain, 0, kDiffBwdDrainNs);
+      mbar_wait_warp(&sh->drain, 0, kDiffBwdDrainNs);
     }
   } else if (warp == 2) {
     // ---------------------------------------------------------- tcgen05 issuer of dP and dQ:
@@ -300,20 +293,17 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
         mma_commit(&sh->dp_full);
         mma_commit(&sh->v_empty[j & 1]);
       };
-      bool ok = mbar_await_warp(&sh->fixed_full, 0, limit_ns) && mbar_await_warp(&sh->v_full[0], 0, limit_ns);
-      if (ok) {
-        tc_fence_after();
-        if (elect_one()) issue_dp(0);
-      }
+      bool ok = mbar_await(&sh->fixed_full, 0, limit_ns);
+      ok = ok && mbar_await(&sh->v_full[0], 0, limit_ns);
+      tc_fence_after();
+      if (ok && elect_one()) issue_dp(0);
       int s = 0;
       uint32_t ph = 0;
       for (int j = 0; ok && j < n; ++j) {
-        if (__any_sync(0xffffffffu, sh->abort_flag) || !mbar_await_warp(&sh->k_full[s], ph, limit_ns) ||
-            (j + 1 < n && !mbar_await_warp(&sh->v_full[(j + 1) & 1], (uint32_t)(((j + 1) >> 1) & 1), limit_ns)) ||
-            !mbar_await_warp(&sh->ds_full, (uint32_t)(j & 1), limit_ns)) {
-          ok = false;
-          break;
-        }
+        ok = ok && mbar_await(&sh->k_full[s], ph, limit_ns);
+        ok = ok && (j + 1 == n || mbar_await(&sh->v_full[(j + 1) & 1], (uint32_t)(((j + 1) >> 1) & 1), limit_ns));
+        ok = ok && mbar_await(&sh->ds_full, (uint32_t)(j & 1), limit_ns);
+        if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
           const uint32_t kt = sbase + C::DQ_OFF_K + s * C::TILE;
@@ -333,9 +323,9 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
         s = s == 2 ? 0 : s + 1;
         ph = s == 0 ? ph ^ 1 : ph;
       }
-      if (!ok) diff_bwd_timeout(sh, status);
+      if (!ok) diff_bwd_timeout(status);
       if (elect_one()) mma_commit(&sh->drain);
-      mbar_await_warp(&sh->drain, 0, kDiffBwdDrainNs);
+      mbar_wait_warp(&sh->drain, 0, kDiffBwdDrainNs);
     }
   } else if (warp >= 4) {
     // one thread a query row and half of the keys of every tile
@@ -346,10 +336,12 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     const uint64_t c2 = f32x2_pack(scale_log2, scale_log2), nl1 = f32x2_pack(-l1, -l1), nl2 = f32x2_pack(-l2, -l2);
     const uint64_t nd1 = f32x2_pack(-D1, -D1), nd2 = f32x2_pack(-D2, -D2);
     uint64_t dl2 = 0;  // (0, 0)
+    const int last = n > 0 ? N - col_idx[c0 + n - 1] * 128 : 0;  // (columns ascend: only the last tile can be short)
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const int valid = N - col_idx[c0 + j] * 128 - 64 * half;  // real keys from this half's first on
-      if (!mbar_await_warp(&sh->s_full, (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
+    for (int j = 0; ok && j < n; ++j) {
+      const int valid = (j + 1 == n ? last : 128) - 64 * half;  // real keys from this half's first on
+      ok = mbar_await(&sh->s_full, (uint32_t)(j & 1), limit_ns);
+      if (!ok) break;
       tc_fence_after();
       // P_1, then P_2: S is released once both are in registers, so that S of the
       // next tile runs beside P_2's exponentials
@@ -367,7 +359,8 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       if (lane == 0) mbar_arrive(&sh->s_read);
 #pragma unroll
       for (int c = 0; c < 2; ++c) diff_exp32(p2[c], c2, nl2, valid - 32 * c);
-      if (!mbar_await_warp(&sh->dp_full, (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
+      ok = mbar_await(&sh->dp_full, (uint32_t)(j & 1), limit_ns);
+      if (!ok) break;
       tc_fence_after();
       // (both chunks of a thread's dP are read before dS takes their place: the
       // first chunk's dS_1 lies over the first chunk, its dS_2 over the second)
@@ -402,9 +395,9 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->ds_full);
     }
-    if (ok && n >= 1) ok = mbar_await_warp(&sh->mm_done, 0, limit_ns);  // the last gradient products
+    ok = ok && (n == 0 || mbar_await(&sh->mm_done, 0, limit_ns));  // the last gradient products
     if (!ok) {
-      diff_bwd_timeout(sh, status);
+      diff_bwd_timeout(status);
     } else {
       tc_fence_after();
       const int row = qt * 128 + r;
@@ -480,7 +473,6 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     mbar_init(&sh->ds_full, 8);
     mbar_init(&sh->mm_done, 1);
     mbar_init(&sh->drain, 3);
-    sh->abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -507,7 +499,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       for (int i = 0; i < 2 * n; ++i) {
         if ((i & 1) == 0) qi = t_col_idx[c0 + (i >> 1)];
         const int s = i % C::STAGES, q0 = qi * 128 + 64 * (i & 1);
-        if (sh->abort_flag || !mbar_await(&sh->ring_empty[s], (uint32_t)((i / C::STAGES) & 1) ^ 1, limit_ns)) {
+        if (!mbar_wait(&sh->ring_empty[s], (uint32_t)((i / C::STAGES) & 1) ^ 1, limit_ns)) {
           ok = false;
           break;
         }
@@ -519,11 +511,11 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
         bulk_load(vec, rows + ((size_t)bh * npad + (size_t)q0) * 4, C::VEC, &sh->ring_full[s]);
         ++loads;
       }
-      if (!ok) diff_bwd_timeout(sh, status);
+      if (!ok) diff_bwd_timeout(status);
       // every copy this thread started lands before the CTA exits
-      mbar_await(&sh->fixed_full, 0, kDiffBwdDrainNs);
+      mbar_wait(&sh->fixed_full, 0, kDiffBwdDrainNs);
       for (int i = (loads > C::STAGES ? loads - C::STAGES : 0); i < loads; ++i)
-        mbar_await(&sh->ring_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), kDiffBwdDrainNs);
+        mbar_wait(&sh->ring_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), kDiffBwdDrainNs);
     }
   } else if (warp < 4) {
     // ---------------------------------------------------------- tcgen05 issuers: S^T of both
@@ -531,17 +523,16 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     // ones before in registers, the gradient products (warp 3) once their operands
     // are written
     if (n > 0) {  // (whole warps; one lane issues)
-      bool ok = mbar_await_warp(&sh->fixed_full, 0, limit_ns);
+      bool ok = mbar_await(&sh->fixed_full, 0, limit_ns);
       for (int i = 0; ok && i < 2 * n; ++i) {
         const int s = i % C::STAGES;
         const uint32_t qs = sbase + C::OFF_RING + s * 2 * C::HALF;
-        if (__any_sync(0xffffffffu, sh->abort_flag) ||
-            !mbar_await_warp(&sh->ring_full[s], (uint32_t)((i / C::STAGES) & 1), limit_ns) ||
-            (warp < 3 && i > 0 && !mbar_await_warp(&sh->s_read, (uint32_t)((i - 1) & 1), limit_ns)) ||
-            (warp == 3 && !mbar_await_warp(&sh->ds_full, (uint32_t)(i & 1), limit_ns))) {
-          ok = false;
-          break;
-        }
+        ok = ok && mbar_await(&sh->ring_full[s], (uint32_t)((i / C::STAGES) & 1), limit_ns);
+        if (warp == 3)
+          ok = ok && mbar_await(&sh->ds_full, (uint32_t)(i & 1), limit_ns);
+        else if (i > 0)
+          ok = ok && mbar_await(&sh->s_read, (uint32_t)((i - 1) & 1), limit_ns);
+        if (!ok) break;
         tc_fence_after();
         if (warp == 1) {
           if (elect_one()) {
@@ -568,10 +559,10 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
           mma_commit(&sh->ring_empty[s]);
         }
       }
-      if (!ok) diff_bwd_timeout(sh, status);
+      if (!ok) diff_bwd_timeout(status);
       // every product has ended before the tensor memory is given back, also when a row warp gave up
       if (elect_one()) mma_commit(&sh->drain);
-      mbar_await_warp(&sh->drain, 0, kDiffBwdDrainNs);
+      mbar_wait_warp(&sh->drain, 0, kDiffBwdDrainNs);
     }
   } else {
     // one thread a key row and half of a step's queries
@@ -581,13 +572,11 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     const uint64_t c2 = f32x2_pack(scale_log2, scale_log2), nlam = f32x2_pack(-lh, -lh);
     const uint64_t minus = f32x2_pack(-1.f, -1.f);
     bool ok = true;
-    for (int i = 0; i < 2 * n; ++i) {
+    for (int i = 0; ok && i < 2 * n; ++i) {
       const int s = i % C::STAGES;
-      if (!mbar_await_warp(&sh->s_full, (uint32_t)(i & 1), limit_ns) ||
-          !mbar_await_warp(&sh->ring_full[s], (uint32_t)((i / C::STAGES) & 1), limit_ns)) {
-        ok = false;
-        break;
-      }
+      ok = mbar_await(&sh->s_full, (uint32_t)(i & 1), limit_ns) &&
+           mbar_await(&sh->ring_full[s], (uint32_t)((i / C::STAGES) & 1), limit_ns);
+      if (!ok) break;
       tc_fence_after();
       const uint32_t vec = sbase + C::OFF_VEC + s * C::VEC + 128 * half;  // lse_1, then + 256 bytes lse_2, D_1, D_2
       uint32_t s1[32], s2[32], g[32];
@@ -629,7 +618,8 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
         }
       }
       // the products of the step before have read the operands' places
-      if (i >= 1 && !mbar_await_warp(&sh->mm_done, (uint32_t)((i - 1) & 1), limit_ns)) { ok = false; break; }
+      ok = i == 0 || mbar_await(&sh->mm_done, (uint32_t)((i - 1) & 1), limit_ns);
+      if (!ok) break;
       tc_fence_after();
       tmem_st16(lane_addr + TM_A + 16 * half, a);
       tmem_st16(lane_addr + TM_DS + 16 * half, z1);
@@ -643,9 +633,9 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->ds_full);
     }
-    if (ok && n >= 1) ok = mbar_await_warp(&sh->mm_done, (uint32_t)((2 * n - 1) & 1), limit_ns);
+    ok = ok && (n == 0 || mbar_await(&sh->mm_done, (uint32_t)((2 * n - 1) & 1), limit_ns));
     if (!ok) {
-      diff_bwd_timeout(sh, status);
+      diff_bwd_timeout(status);
     } else {
       tc_fence_after();
       const int row = kt * 128 + r;

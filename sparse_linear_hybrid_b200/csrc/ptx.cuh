@@ -74,22 +74,26 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, u
   return __all_sync(0xffffffffu, ok);
 }
 
-// mbar_wait and mbar_wait_warp that only look when the limit is 0: try_wait may
-// suspend the thread for a while and find the phase complete after all.
+// Bounded wait of a converged warp; the same answer in all lanes.  After false the
+// caller arrives, commits and issues nothing more: a stage given back before its
+// copy has landed would let the CTA end with the copy in flight.  With a limit of
+// 0 a wait that is not satisfied yet fails (test_wait: try_wait may suspend the
+// thread and find the phase complete after all).
 __device__ __forceinline__ bool mbar_await(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-  if (limit_ns != 0) return mbar_wait(bar, parity, limit_ns);
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool mbar_await_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-  const bool ok = mbar_await(bar, parity, limit_ns);
+  bool ok;
+  if (limit_ns != 0) {
+    ok = mbar_try_wait(bar, parity) || mbar_wait(bar, parity, limit_ns);
+  } else {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    ok = done != 0;
+  }
   return __all_sync(0xffffffffu, ok);
 }
 
