@@ -6,17 +6,18 @@
 // One CTA takes one 128-row query tile of one (b, h) and walks its kept key
 // tiles; both maps read the same K and V tiles.
 //
-// Tensor memory (512 columns): S_1 [0,128), S_2 [128,256), O_1 [256,256+d),
-// O_2 [384,384+d); P_m as bf16 over the first 64 columns of S_m, so S_m of the
-// next tile follows P_m V in the issue order.  The maps alternate: while the four
-// softmax warps of map 1 work, the tensor cores run P_2 V and S_2 of the next
-// tile, and the other way round.
+// Tensor memory (512 columns): O_1 [256,256+d), O_2 [384,384+d), and for map m two
+// score buffers of 64 keys, [128 m, +64) and [128 m + 64, +64).  A step is 64 keys:
+// P_m as bf16 takes the place of the step's scores, and the scores two steps on
+// follow P_m V in the issue order, so a map's softmax warps work on one buffer
+// while the tensor cores work on the other.  (Whole tiles of 128 keys in one
+// buffer each: 1,019 us against ... at 1.3B; products of 64 keys from shared memory
+// run at 48 cycles, not 32, but nobody waits for them.)
 // Warp roles, 384 threads: warp 0 TMA producer (K and V rings of three tiles),
 // warp 1 tcgen05 issuer and owner of the tensor memory, warps 4-7 softmax of map
-// 1 and warps 8-11 of map 2, one thread a query row.  P enters its
-// product as bf16 (2^-9 of each weight, a fifth of the output's own rounding in a
-// row of many keys); the row sum and the log-sum-exp add the unrounded p.
-// At the end the two warp groups
+// 1 and warps 8-11 of map 2, one thread a query row.  P enters its product as
+// bf16 (a choice: 2^-9 of each weight; the output's own rounding is as large); the
+// row sum and the log-sum-exp add the unrounded p.  At the end the two warp groups
 // exchange the row sums and each writes half of the features of its row.
 //
 // Bound by the exponentials: 2 x 128 x 128 a tile pair, 16 a clock and SM on the
@@ -37,8 +38,9 @@ constexpr float kLn2 = 0.69314718055994531f;
 struct DiffShared {
   uint64_t q_full;
   uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
-  uint64_t s_full[2];   // per map: S of the current tile is in tensor memory (and the P V before it is done)
-  uint64_t p_full[2];   // per map: the four softmax warps have written P
+  uint64_t s_full[2][2];  // per map and buffer: the scores of a step are in tensor memory
+  uint64_t p_full[2][2];  // per map and buffer: the four softmax warps have written P of a step (they may be a step ahead)
+  uint64_t pv_done[2];    // per map: P V of a step is done
   uint64_t o_full;      // every product is done
   uint64_t drain;
   uint32_t tmem_base;
@@ -59,7 +61,7 @@ struct DiffCfg {
   // at least 120 KB so that one CTA (and its 512 TMEM columns) owns the SM
   static constexpr int SMEM = SMEM_USED > 122880 ? SMEM_USED : 122880;
   static constexpr uint32_t TM_S = 0, TM_O = 256;       // + 128 per map
-  static constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false);
+  static constexpr uint32_t IDESC_S = idesc_bf16(128, 64, false, false);  // 64 keys
   static constexpr uint32_t IDESC_PV = idesc_bf16(128, D, false, true);
   static_assert(SMEM <= 232448, "shared memory budget");
 };
@@ -155,12 +157,17 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(diff_smem_raw) + 1023) & ~uintptr_t(1023));
   DiffShared* sh = reinterpret_cast<DiffShared*>(smem + C::OFF_BAR);
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t polls = polls_of(limit_ns);
+  const int warp = warp_uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int qt = blockIdx.x % nb, bh = blockIdx.x / nb, b = bh / heads, h = bh % heads;
   const int mrow = (mask_per_bh ? bh : h) * nb + qt;
   const int mask_rows = (mask_per_bh ? (int)(gridDim.x / nb) : heads) * nb;
-  const int c0 = row_ptr[mrow];
-  const int n = debug_row_ok(row_ptr, col_idx, mrow, mask_rows, nb, true, status) ? row_ptr[mrow + 1] - c0 : 0;
+  const int c0 = warp_uniform(row_ptr[mrow]);
+  const int n = warp_uniform(debug_row_ok(row_ptr, col_idx, mrow, mask_rows, nb, true, status) ? row_ptr[mrow + 1] - c0 : 0);
+
+  // steps of 64 keys; columns ascend, so only the last tile can be short
+  const int last = warp_uniform(n > 0 ? min(128, N - col_idx[c0 + n - 1] * 128) : 0);
+  const int steps = 2 * n - (n > 0 && last <= 64 ? 1 : 0);
 
   if (threadIdx.x == 0) {
     mbar_init(&sh->q_full, 1);
@@ -171,8 +178,11 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       mbar_init(&sh->v_empty[s], 1);
     }
     for (int m = 0; m < 2; ++m) {
-      mbar_init(&sh->s_full[m], 1);
-      mbar_init(&sh->p_full[m], 4);
+      mbar_init(&sh->s_full[m][0], 1);
+      mbar_init(&sh->s_full[m][1], 1);
+      mbar_init(&sh->pv_done[m], 1);
+      mbar_init(&sh->p_full[m][0], 4);
+      mbar_init(&sh->p_full[m][1], 4);
     }
     mbar_init(&sh->o_full, 1);
     mbar_init(&sh->drain, 1);
@@ -199,11 +209,11 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       for (int j = 0; j < n; ++j) {
         const int s = j % C::STAGES, col = col_idx[c0 + j];
         const uint32_t ph = (uint32_t)((j / C::STAGES) & 1);
-        if (!mbar_wait(&sh->k_empty[s], ph ^ 1, limit_ns)) { ok = false; break; }
+        if (!mbar_await_one(&sh->k_empty[s], ph ^ 1, polls)) { ok = false; break; }
         mbar_arrive_expect_tx(&sh->k_full[s], C::TILE);
         tma_load_4d(smem + C::OFF_K + s * C::TILE, &tm_k, &sh->k_full[s], 0, col * 128, h * C::DCH, b);
         ++kl;
-        if (!mbar_wait(&sh->v_empty[s], ph ^ 1, limit_ns)) { ok = false; break; }
+        if (!mbar_await_one(&sh->v_empty[s], ph ^ 1, polls)) { ok = false; break; }
         mbar_arrive_expect_tx(&sh->v_full[s], C::TILE);
         tma_load_4d(smem + C::OFF_V + s * C::TILE, &tm_v, &sh->v_full[s], 0, col * 128, h * C::DCH, b);
         ++vl;
@@ -219,57 +229,70 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
   } else if (warp == 1) {
     // ---------------------------------------------------------- tcgen05 issuer
     if (n > 0) {  // (the whole warp; one lane issues)
-      // S_m from stage s: the k-steps of the map's half of the features
-      auto issue_s = [&](int m, int s) {
-        const uint32_t q_s = sbase + C::OFF_Q, kt = sbase + C::OFF_K + s * C::TILE;
+      // scores of map m and step u (keys [64 (u & 1), +64) of the tile in stage s): the
+      // k-steps of the map's half of the features
+      auto issue_s = [&](int m, int u, int s) {
+        const uint32_t q_s = sbase + C::OFF_Q, kt = sbase + C::OFF_K + s * C::TILE + (u & 1) * 8192;
 #pragma unroll
         for (int kk = 0; kk < D / 32; ++kk) {
           const int f = m * (D / 32) + kk;
           const uint32_t off = (f / 4) * 16384 + (f % 4) * 32;
-          mma_bf16_ss(tmem + C::TM_S + 128 * m, sw128_desc(q_s + off, 16, 1024), sw128_desc(kt + off, 16, 1024),
-                      C::IDESC_S, kk > 0 ? 1u : 0u);
+          mma_bf16_ss(tmem + C::TM_S + 128 * m + 64 * (u & 1), sw128_desc(q_s + off, 16, 1024),
+                      sw128_desc(kt + off, 16, 1024), C::IDESC_S, kk > 0 ? 1u : 0u);
         }
-        mma_commit(&sh->s_full[m]);
-        if (m == 1) mma_commit(&sh->k_empty[s]);
+        mma_commit(&sh->s_full[m][u & 1]);
       };
-      bool ok = mbar_await(&sh->q_full, 0, limit_ns) && mbar_await(&sh->k_full[0], 0, limit_ns);
-      if (ok) {
-        tc_fence_after();
-        if (elect_one()) {
-          issue_s(0, 0);
-          issue_s(1, 0);
+      bool ok = limit_ns != 0;
+      mbar_await(&sh->q_full, 0, polls, ok);
+      mbar_await(&sh->k_full[0], 0, polls, ok);
+      tc_fence_after();
+      if (elect_one() && ok) {
+        issue_s(0, 0, 0);
+        issue_s(1, 0, 0);
+        if (steps > 1) {
+          issue_s(0, 1, 0);
+          issue_s(1, 1, 0);
         }
+        mma_commit(&sh->k_empty[0]);
       }
       int s = 0;
-      uint32_t ph = 0;  // stage and parity of tile j
-      for (int j = 0; ok && j < n; ++j) {
+      uint32_t ph = 0;  // stage and parity of the step's tile
+      for (int u = 0; u < steps; ++u) {
         const int s1 = s + 1 == C::STAGES ? 0 : s + 1;
         const uint32_t ph1 = s1 == 0 ? ph ^ 1 : ph;
-        ok = mbar_await(&sh->v_full[s], ph, limit_ns) &&
-             (j + 1 == n || mbar_await(&sh->k_full[s1], ph1, limit_ns));
+        const bool next = u + 2 < steps;  // the step that takes this one's buffer
+        if ((u & 1) == 0) {
+          mbar_await(&sh->v_full[s], ph, polls, ok);
+          if (next) mbar_await(&sh->k_full[s1], ph1, polls, ok);
+        }
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          ok = ok && mbar_await(&sh->p_full[m], (uint32_t)(j & 1), limit_ns);
-          if (!ok) break;
+          mbar_await(&sh->p_full[m][u & 1], (uint32_t)((u >> 1) & 1), polls, ok);
           tc_fence_after();
-          if (elect_one()) {
-            const uint32_t vt = sbase + C::OFF_V + s * C::TILE;
+          if (elect_one() && ok) {
+            const uint32_t vt = sbase + C::OFF_V + s * C::TILE + (u & 1) * 8192;
+            const uint32_t pt = tmem + C::TM_S + 128 * m + 64 * (u & 1);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_bf16_ts(tmem + C::TM_O + 128 * m, tmem + C::TM_S + 128 * m + kk * 8,
-                          sw128_desc(vt + kk * 2048, 16384, 1024), C::IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
-            if (m == 1) mma_commit(&sh->v_empty[s]);
-            if (j + 1 < n) issue_s(m, s1);  // over P, behind the product that reads it
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_ts(tmem + C::TM_O + 128 * m, pt + kk * 8, sw128_desc(vt + kk * 2048, 16384, 1024), C::IDESC_PV,
+                          (u > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(&sh->pv_done[m]);
+            if (m == 1 && ((u & 1) == 1 || u + 1 == steps)) mma_commit(&sh->v_empty[s]);
+            if (next) {
+              issue_s(m, u + 2, s1);  // over P, behind the product that reads it
+              if (m == 1 && ((u & 1) == 1 || u + 3 == steps)) mma_commit(&sh->k_empty[s1]);
+            }
           }
         }
-        s = s1;
-        ph = ph1;
+        if (u & 1) {
+          s = s1;
+          ph = ph1;
+        }
       }
-      if (ok) {
-        if (elect_one()) mma_commit(&sh->o_full);
-      } else {
-        diff_timeout(sh, status);
-      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (elect_one() && ok) mma_commit(&sh->o_full);
+      if (!ok) diff_timeout(sh, status);
+      __syncwarp();
       // every product has ended before the tensor memory is given back, also when a softmax warp gave up
       if (elect_one()) mma_commit(&sh->drain);
       mbar_wait_warp(&sh->drain, 0, kDiffDrainNs);
@@ -281,61 +304,53 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     const uint32_t s_addr = lane_addr + C::TM_S + 128 * m, o_addr = lane_addr + C::TM_O + 128 * m;
     const uint64_t c2 = f32x2_pack(scale_log2, scale_log2);
     float m_ref = -INFINITY, l = 0.f;
-    const int last = n > 0 ? N - col_idx[c0 + n - 1] * 128 : 0;  // (columns ascend: only the last tile can be short)
-    bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const int valid = j + 1 == n ? last : 128;  // real keys of the tile
-      if (!mbar_await(&sh->s_full[m], (uint32_t)(j & 1), limit_ns)) { ok = false; break; }
+    bool ok = limit_ns != 0;
+    for (int u = 0; u < steps; ++u) {
+      const uint32_t buf = s_addr + 64 * (u & 1);
+      const int valid = u + 1 == steps ? last - 64 * (u & 1) : 64;  // real keys of the step
+      mbar_await(&sh->s_full[m][u & 1], (uint32_t)((u >> 1) & 1), polls, ok);
       tc_fence_after();
-      // The reference is the first tile's maximum, and later tiles' exponentials
+      // The reference is the first step's maximum, and later steps' exponentials
       // are taken against it without looking for their own: fp32 and bf16 hold p
       // and its sums up to far above 2^60, and a row's precision does not depend
-      // on their common factor.  Only when 64 keys' sum passes 2^60 does the row
-      // take their maximum as its new reference, with O, l and the first keys' P
-      // scaled down and the exponentials taken again (the scores are still there).
-      if (j == 0) m_ref = fmaxf(row_max(s_addr, valid), row_max(s_addr + 64, valid - 64));
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        uint32_t pk[32];
-        float rs = softmax_pass(s_addr + 64 * hf, valid - 64 * hf, c2, -m_ref * scale_log2, pk);
-        const bool grown = rs > kDiffGrown;
-        if (__any_sync(0xffffffffu, grown)) {
-          const float mt = row_max(s_addr + 64 * hf, valid - 64 * hf);
-          float alpha = 1.f;
-          if (grown) {
-            alpha = ex2_approx((m_ref - mt) * scale_log2);
-            m_ref = mt;
-          }
-          l *= alpha;
-          if (j > 0) {  // (the product that wrote O last came before S of this tile)
+      // on their common factor.  Only when a step's sum passes 2^60 does the row
+      // take the step's maximum as its new reference, with O and l scaled down and
+      // the exponentials taken again (the scores are still there).
+      if (u == 0) m_ref = row_max(buf, valid);
+      uint32_t pk[32];
+      float rs = softmax_pass(buf, valid, c2, -m_ref * scale_log2, pk);
+      const bool grown = rs > kDiffGrown;
+      if (__any_sync(0xffffffffu, grown)) {
+        const float mt = row_max(buf, valid);
+        float alpha = 1.f;
+        if (grown) {
+          alpha = ex2_approx((m_ref - mt) * scale_log2);
+          m_ref = mt;
+        }
+        l *= alpha;
+        if (u > 0) {
+          mbar_await(&sh->pv_done[m], (uint32_t)((u - 1) & 1), polls, ok);
+          tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              tmem_ld32(o_addr + 32 * c, pk);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) pk[i] = __float_as_uint(__uint_as_float(pk[i]) * alpha);
-              tmem_st32(o_addr + 32 * c, pk);
-            }
-          }
-          if (hf == 1) {
-            tmem_ld32(s_addr, pk);
+          for (int c = 0; c < D / 32; ++c) {
+            tmem_ld32(o_addr + 32 * c, pk);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              pk[i] = pack_bf16x2(bf16_lo_to_f32(pk[i]) * alpha, bf16_hi_to_f32(pk[i]) * alpha);
-            tmem_st32(s_addr, pk);
+            for (int i = 0; i < 32; ++i) pk[i] = __float_as_uint(__uint_as_float(pk[i]) * alpha);
+            tmem_st32(o_addr + 32 * c, pk);
           }
-          rs = softmax_pass(s_addr + 64 * hf, valid - 64 * hf, c2, -m_ref * scale_log2, pk);
         }
-        l += rs;
-        tmem_st32(s_addr + 32 * hf, pk);  // over scores that have been read
+        rs = softmax_pass(buf, valid, c2, -m_ref * scale_log2, pk);
       }
+      l += rs;
+      tmem_st32(buf, pk);  // over scores that have been read
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->p_full[m]);
+      if (lane == 0 && ok) mbar_arrive(&sh->p_full[m][u & 1]);
     }
-    if (ok && n > 0) ok = mbar_await(&sh->o_full, 0, limit_ns);
+    if (n > 0) mbar_await(&sh->o_full, 0, polls, ok);
+    ok = __all_sync(0xffffffffu, ok);
     if (!ok) diff_timeout(sh, status);
     const int row = qt * 128 + r;
     if (TRAIN && ok && row < N) {
@@ -348,7 +363,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     // features [m D/2, m D/2 + D/2) of this row: out = O_1 / l_1 - lam O_2 / l_2
     const float lh = lambda_of(lam, lam_bf16, h);
     const float i1 = n > 0 ? 1.f / sh->sum[0][r] : 0.f, i2 = n > 0 ? 1.f / sh->sum[1][r] : 0.f;
-    if (n == 0) mbar_await(&sh->q_full, 0, limit_ns);  // the Q buffer is written over: its load must have landed
+    if (n == 0) mbar_await(&sh->q_full, 0, polls, ok);  // the Q buffer is written over: its load must have landed
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       const int f0 = m * (D / 2) + 32 * c;  // 32 features

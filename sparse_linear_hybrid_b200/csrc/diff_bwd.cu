@@ -201,12 +201,13 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(diff_smem_raw) + 1023) & ~uintptr_t(1023));
   DiffBwdShared* sh = reinterpret_cast<DiffBwdShared*>(smem + C::DQ_OFF_BAR);
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t polls = polls_of(limit_ns);
+  const int warp = warp_uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int qt = blockIdx.x % nb, bh = blockIdx.x / nb, b = bh / heads, h = bh % heads;
   const int mrow = (mask_per_bh ? bh : h) * nb + qt;
   const int mask_rows = (mask_per_bh ? (int)(gridDim.x / nb) : heads) * nb;
-  const int c0 = row_ptr[mrow];
-  const int n = debug_row_ok(row_ptr, col_idx, mrow, mask_rows, nb, true, status) ? row_ptr[mrow + 1] - c0 : 0;
+  const int c0 = warp_uniform(row_ptr[mrow]);
+  const int n = warp_uniform(debug_row_ok(row_ptr, col_idx, mrow, mask_rows, nb, true, status) ? row_ptr[mrow + 1] - c0 : 0);
 
   if (threadIdx.x == 0) {
     mbar_init(&sh->fixed_full, 1);
@@ -241,11 +242,11 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       // K_j is free once the gradient products of tile j have read it, V_j once dP_j is done
       for (int j = 0; j < n; ++j) {
         const int col = col_idx[c0 + j], ks = j % 3, vs = j & 1;
-        if (!mbar_wait(&sh->k_empty[ks], (uint32_t)((j / 3) & 1) ^ 1, limit_ns)) { ok = false; break; }
+        if (!mbar_await_one(&sh->k_empty[ks], (uint32_t)((j / 3) & 1) ^ 1, polls)) { ok = false; break; }
         mbar_arrive_expect_tx(&sh->k_full[ks], C::TILE);
         tma_load_4d(smem + C::DQ_OFF_K + ks * C::TILE, &tm_k, &sh->k_full[ks], 0, col * 128, h * C::DCH, b);
         ++kl;
-        if (!mbar_wait(&sh->v_empty[vs], (uint32_t)((j >> 1) & 1) ^ 1, limit_ns)) { ok = false; break; }
+        if (!mbar_await_one(&sh->v_empty[vs], (uint32_t)((j >> 1) & 1) ^ 1, polls)) { ok = false; break; }
         mbar_arrive_expect_tx(&sh->v_full[vs], C::TILE);
         tma_load_4d(smem + C::DQ_OFF_V + vs * C::TILE, &tm_v, &sh->v_full[vs], 0, col * 128, h * C::DCH, b);
         ++vl;
@@ -262,15 +263,15 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     // ---------------------------------------------------------- tcgen05 issuer of S: of the
     // next tile as soon as the row warps hold S in registers
     if (n > 0) {  // (the whole warp; one lane issues)
-      bool ok = mbar_await(&sh->fixed_full, 0, limit_ns);
+      bool ok = limit_ns != 0;
+      mbar_await(&sh->fixed_full, 0, polls, ok);
       int s = 0;
       uint32_t ph = 0;  // K stage and its parity
-      for (int j = 0; ok && j < n; ++j) {
-        ok = ok && mbar_await(&sh->k_full[s], ph, limit_ns);
-        ok = ok && (j == 0 || mbar_await(&sh->s_read, (uint32_t)((j - 1) & 1), limit_ns));
-        if (!ok) break;
+      for (int j = 0; j < n; ++j) {
+        mbar_await(&sh->k_full[s], ph, polls, ok);
+        if (j > 0) mbar_await(&sh->s_read, (uint32_t)((j - 1) & 1), polls, ok);
         tc_fence_after();
-        if (elect_one()) {
+        if (elect_one() && ok) {
           const uint32_t kt = sbase + C::DQ_OFF_K + s * C::TILE;
           mma_steps<D / 32>(tmem + TM_S, q_s, kt, 0, C::IDESC_S);
           mma_steps<D / 32>(tmem + TM_S + 128, q_s, kt, D / 32, C::IDESC_S);
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
         s = s == 2 ? 0 : s + 1;
         ph = s == 0 ? ph ^ 1 : ph;
       }
-      if (!ok) diff_bwd_timeout(status);
+      if (!__all_sync(0xffffffffu, ok)) diff_bwd_timeout(status);
       // every product has ended before the tensor memory is given back, also when a row warp gave up
       if (elect_one()) mma_commit(&sh->drain);
       mbar_wait_warp(&sh->drain, 0, kDiffBwdDrainNs);
@@ -293,19 +294,19 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
         mma_commit(&sh->dp_full);
         mma_commit(&sh->v_empty[j & 1]);
       };
-      bool ok = mbar_await(&sh->fixed_full, 0, limit_ns);
-      ok = ok && mbar_await(&sh->v_full[0], 0, limit_ns);
+      bool ok = limit_ns != 0;
+      mbar_await(&sh->fixed_full, 0, polls, ok);
+      mbar_await(&sh->v_full[0], 0, polls, ok);
       tc_fence_after();
-      if (ok && elect_one()) issue_dp(0);
+      if (elect_one() && ok) issue_dp(0);
       int s = 0;
       uint32_t ph = 0;
-      for (int j = 0; ok && j < n; ++j) {
-        ok = ok && mbar_await(&sh->k_full[s], ph, limit_ns);
-        ok = ok && (j + 1 == n || mbar_await(&sh->v_full[(j + 1) & 1], (uint32_t)(((j + 1) >> 1) & 1), limit_ns));
-        ok = ok && mbar_await(&sh->ds_full, (uint32_t)(j & 1), limit_ns);
-        if (!ok) break;
+      for (int j = 0; j < n; ++j) {
+        mbar_await(&sh->k_full[s], ph, polls, ok);
+        if (j + 1 < n) mbar_await(&sh->v_full[(j + 1) & 1], (uint32_t)(((j + 1) >> 1) & 1), polls, ok);
+        mbar_await(&sh->ds_full, (uint32_t)(j & 1), polls, ok);
         tc_fence_after();
-        if (elect_one()) {
+        if (elect_one() && ok) {
           const uint32_t kt = sbase + C::DQ_OFF_K + s * C::TILE;
 #pragma unroll
           for (int m = 0; m < 2; ++m)
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
         s = s == 2 ? 0 : s + 1;
         ph = s == 0 ? ph ^ 1 : ph;
       }
-      if (!ok) diff_bwd_timeout(status);
+      if (!__all_sync(0xffffffffu, ok)) diff_bwd_timeout(status);
       if (elect_one()) mma_commit(&sh->drain);
       mbar_wait_warp(&sh->drain, 0, kDiffBwdDrainNs);
     }
@@ -336,12 +337,11 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     const uint64_t c2 = f32x2_pack(scale_log2, scale_log2), nl1 = f32x2_pack(-l1, -l1), nl2 = f32x2_pack(-l2, -l2);
     const uint64_t nd1 = f32x2_pack(-D1, -D1), nd2 = f32x2_pack(-D2, -D2);
     uint64_t dl2 = 0;  // (0, 0)
-    const int last = n > 0 ? N - col_idx[c0 + n - 1] * 128 : 0;  // (columns ascend: only the last tile can be short)
-    bool ok = true;
-    for (int j = 0; ok && j < n; ++j) {
+    const int last = warp_uniform(n > 0 ? N - col_idx[c0 + n - 1] * 128 : 0);  // (columns ascend: only the last tile can be short)
+    bool ok = limit_ns != 0;
+    for (int j = 0; j < n; ++j) {
       const int valid = (j + 1 == n ? last : 128) - 64 * half;  // real keys from this half's first on
-      ok = mbar_await(&sh->s_full, (uint32_t)(j & 1), limit_ns);
-      if (!ok) break;
+      mbar_await(&sh->s_full, (uint32_t)(j & 1), polls, ok);
       tc_fence_after();
       // P_1, then P_2: S is released once both are in registers, so that S of the
       // next tile runs beside P_2's exponentials
@@ -356,11 +356,10 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->s_read);
+      if (lane == 0 && ok) mbar_arrive(&sh->s_read);
 #pragma unroll
       for (int c = 0; c < 2; ++c) diff_exp32(p2[c], c2, nl2, valid - 32 * c);
-      ok = mbar_await(&sh->dp_full, (uint32_t)(j & 1), limit_ns);
-      if (!ok) break;
+      mbar_await(&sh->dp_full, (uint32_t)(j & 1), polls, ok);
       tc_fence_after();
       // (both chunks of a thread's dP are read before dS takes their place: the
       // first chunk's dS_1 lies over the first chunk, its dS_2 over the second)
@@ -393,9 +392,10 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->ds_full);
+      if (lane == 0 && ok) mbar_arrive(&sh->ds_full);
     }
-    ok = ok && (n == 0 || mbar_await(&sh->mm_done, 0, limit_ns));  // the last gradient products
+    if (n > 0) mbar_await(&sh->mm_done, 0, polls, ok);  // the last gradient products
+    ok = __all_sync(0xffffffffu, ok);
     if (!ok) {
       diff_bwd_timeout(status);
     } else {
@@ -457,13 +457,14 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(diff_smem_raw) + 1023) & ~uintptr_t(1023));
   DiffBwdShared* sh = reinterpret_cast<DiffBwdShared*>(smem + C::OFF_BAR);
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t polls = polls_of(limit_ns);
+  const int warp = warp_uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int kt = blockIdx.x % nb, bh = blockIdx.x / nb, b = bh / heads, h = bh % heads;
   const int mrow = (mask_per_bh ? bh : h) * nb + kt;
   const int mask_rows = (mask_per_bh ? (int)(gridDim.x / nb) : heads) * nb;
-  const int c0 = t_row_ptr[mrow];
-  const int n =
-      debug_row_ok(t_row_ptr, t_col_idx, mrow, mask_rows, nb, true, status) ? t_row_ptr[mrow + 1] - c0 : 0;
+  const int c0 = warp_uniform(t_row_ptr[mrow]);
+  const int n = warp_uniform(
+      debug_row_ok(t_row_ptr, t_col_idx, mrow, mask_rows, nb, true, status) ? t_row_ptr[mrow + 1] - c0 : 0);
 
   if (threadIdx.x == 0) {
     mbar_init(&sh->fixed_full, 1);
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       for (int i = 0; i < 2 * n; ++i) {
         if ((i & 1) == 0) qi = t_col_idx[c0 + (i >> 1)];
         const int s = i % C::STAGES, q0 = qi * 128 + 64 * (i & 1);
-        if (!mbar_wait(&sh->ring_empty[s], (uint32_t)((i / C::STAGES) & 1) ^ 1, limit_ns)) {
+        if (!mbar_await_one(&sh->ring_empty[s], (uint32_t)((i / C::STAGES) & 1) ^ 1, polls)) {
           ok = false;
           break;
         }
@@ -523,29 +524,29 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     // ones before in registers, the gradient products (warp 3) once their operands
     // are written
     if (n > 0) {  // (whole warps; one lane issues)
-      bool ok = mbar_await(&sh->fixed_full, 0, limit_ns);
-      for (int i = 0; ok && i < 2 * n; ++i) {
+      bool ok = limit_ns != 0;
+      mbar_await(&sh->fixed_full, 0, polls, ok);
+      for (int i = 0; i < 2 * n; ++i) {
         const int s = i % C::STAGES;
         const uint32_t qs = sbase + C::OFF_RING + s * 2 * C::HALF;
-        ok = ok && mbar_await(&sh->ring_full[s], (uint32_t)((i / C::STAGES) & 1), limit_ns);
+        mbar_await(&sh->ring_full[s], (uint32_t)((i / C::STAGES) & 1), polls, ok);
         if (warp == 3)
-          ok = ok && mbar_await(&sh->ds_full, (uint32_t)(i & 1), limit_ns);
+          mbar_await(&sh->ds_full, (uint32_t)(i & 1), polls, ok);
         else if (i > 0)
-          ok = ok && mbar_await(&sh->s_read, (uint32_t)((i - 1) & 1), limit_ns);
-        if (!ok) break;
+          mbar_await(&sh->s_read, (uint32_t)((i - 1) & 1), polls, ok);
         tc_fence_after();
         if (warp == 1) {
-          if (elect_one()) {
+          if (elect_one() && ok) {
             mma_steps<D / 32>(tmem + TM_S, k_s, qs, 0, C::IDESC_SH, 8192);
             mma_steps<D / 32>(tmem + TM_S + 64, k_s, qs, D / 32, C::IDESC_SH, 8192);
             mma_commit(&sh->s_full);
           }
         } else if (warp == 2) {
-          if (elect_one()) {
+          if (elect_one() && ok) {
             mma_steps<D / 16>(tmem + TM_DP, v_s, qs + C::HALF, 0, C::IDESC_SH, 8192);
             mma_commit(&sh->s_full);
           }
-        } else if (elect_one()) {
+        } else if (elect_one() && ok) {
           const uint32_t ds_s = sbase + C::OFF_DS;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
           mma_commit(&sh->ring_empty[s]);
         }
       }
-      if (!ok) diff_bwd_timeout(status);
+      if (!__all_sync(0xffffffffu, ok)) diff_bwd_timeout(status);
       // every product has ended before the tensor memory is given back, also when a row warp gave up
       if (elect_one()) mma_commit(&sh->drain);
       mbar_wait_warp(&sh->drain, 0, kDiffBwdDrainNs);
@@ -571,12 +572,11 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     const float lh = diff_lambda(lam, lam_bf16, h);
     const uint64_t c2 = f32x2_pack(scale_log2, scale_log2), nlam = f32x2_pack(-lh, -lh);
     const uint64_t minus = f32x2_pack(-1.f, -1.f);
-    bool ok = true;
-    for (int i = 0; ok && i < 2 * n; ++i) {
+    bool ok = limit_ns != 0;
+    for (int i = 0; i < 2 * n; ++i) {
       const int s = i % C::STAGES;
-      ok = mbar_await(&sh->s_full, (uint32_t)(i & 1), limit_ns) &&
-           mbar_await(&sh->ring_full[s], (uint32_t)((i / C::STAGES) & 1), limit_ns);
-      if (!ok) break;
+      mbar_await(&sh->s_full, (uint32_t)(i & 1), polls, ok);
+      mbar_await(&sh->ring_full[s], (uint32_t)((i / C::STAGES) & 1), polls, ok);
       tc_fence_after();
       const uint32_t vec = sbase + C::OFF_VEC + s * C::VEC + 128 * half;  // lse_1, then + 256 bytes lse_2, D_1, D_2
       uint32_t s1[32], s2[32], g[32];
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->s_read);
+      if (lane == 0 && ok) mbar_arrive(&sh->s_read);
       uint32_t a[16], z1[16], z2[16];
 #pragma unroll
       for (int k = 0; k < 16; k += 2) {
@@ -618,8 +618,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
         }
       }
       // the products of the step before have read the operands' places
-      ok = i == 0 || mbar_await(&sh->mm_done, (uint32_t)((i - 1) & 1), limit_ns);
-      if (!ok) break;
+      if (i > 0) mbar_await(&sh->mm_done, (uint32_t)((i - 1) & 1), polls, ok);
       tc_fence_after();
       tmem_st16(lane_addr + TM_A + 16 * half, a);
       tmem_st16(lane_addr + TM_DS + 16 * half, z1);
@@ -631,9 +630,10 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->ds_full);
+      if (lane == 0 && ok) mbar_arrive(&sh->ds_full);
     }
-    ok = ok && (n == 0 || mbar_await(&sh->mm_done, (uint32_t)((2 * n - 1) & 1), limit_ns));
+    if (n > 0) mbar_await(&sh->mm_done, (uint32_t)((2 * n - 1) & 1), polls, ok);
+    ok = __all_sync(0xffffffffu, ok);
     if (!ok) {
       diff_bwd_timeout(status);
     } else {
