@@ -173,9 +173,9 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     mbar_init(&sh->q_full, 1);
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&sh->k_full[s], 1);
-      mbar_init(&sh->k_empty[s], 1);
+      mbar_init(&sh->k_empty[s], 2);  // both maps' products
       mbar_init(&sh->v_full[s], 1);
-      mbar_init(&sh->v_empty[s], 1);
+      mbar_init(&sh->v_empty[s], 2);
     }
     for (int m = 0; m < 2; ++m) {
       mbar_init(&sh->s_full[m][0], 1);
@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       mbar_init(&sh->p_full[m][0], 4);
       mbar_init(&sh->p_full[m][1], 4);
     }
-    mbar_init(&sh->o_full, 1);
-    mbar_init(&sh->drain, 1);
+    mbar_init(&sh->o_full, 2);
+    mbar_init(&sh->drain, 2);
     sh->abort_flag = 0;
     fence_mbar_init();
   }
@@ -226,20 +226,21 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       for (int i = (vl > C::STAGES ? vl - C::STAGES : 0); i < vl; ++i)
         mbar_wait(&sh->v_full[i % C::STAGES], (uint32_t)((i / C::STAGES) & 1), kDiffDrainNs);
     }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------- tcgen05 issuer
+  } else if (warp <= 2) {
+    // ---------------------------------------------------------- tcgen05 issuer of map m
     if (n > 0) {  // (the whole warp; one lane issues)
-      // scores of map m and step u (keys [64 (u & 1), +64) of the tile in stage s): the
-      // k-steps of the map's half of the features
-      auto issue_s = [&](int m, int u, int s) {
-        const uint32_t q_s = sbase + C::OFF_Q, kt = sbase + C::OFF_K + s * C::TILE + (u & 1) * 8192;
+      const int m = warp - 1;
+      const uint32_t s_t = tmem + C::TM_S + 128 * m, o_t = tmem + C::TM_O + 128 * m;
+      // the map's half of the features: chunk m of 64 at d = 128, bytes [64 m, +64) of a row at d = 64
+      const uint32_t half = (D == 128 ? 16384u : 64u) * m;
+      const uint32_t q_s = sbase + C::OFF_Q + half, k_s = sbase + C::OFF_K + half;
+      // scores of step u: keys [64 (u & 1), +64) of the tile in stage s
+      auto issue_s = [&](int u, int s) {
+        const uint32_t kt = k_s + s * C::TILE + (u & 1) * 8192;
 #pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk) {
-          const int f = m * (D / 32) + kk;
-          const uint32_t off = (f / 4) * 16384 + (f % 4) * 32;
-          mma_bf16_ss(tmem + C::TM_S + 128 * m + 64 * (u & 1), sw128_desc(q_s + off, 16, 1024),
-                      sw128_desc(kt + off, 16, 1024), C::IDESC_S, kk > 0 ? 1u : 0u);
-        }
+        for (int kk = 0; kk < D / 32; ++kk)
+          mma_bf16_ss(s_t + 64 * (u & 1), sw128_desc(q_s + 32 * kk, 16, 1024), sw128_desc(kt + 32 * kk, 16, 1024),
+                      C::IDESC_S, kk > 0 ? 1u : 0u);
         mma_commit(&sh->s_full[m][u & 1]);
       };
       bool ok = limit_ns != 0;
@@ -247,12 +248,8 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       mbar_await(&sh->k_full[0], 0, polls, ok);
       tc_fence_after();
       if (elect_one() && ok) {
-        issue_s(0, 0, 0);
-        issue_s(1, 0, 0);
-        if (steps > 1) {
-          issue_s(0, 1, 0);
-          issue_s(1, 1, 0);
-        }
+        issue_s(0, 0);
+        if (steps > 1) issue_s(1, 0);
         mma_commit(&sh->k_empty[0]);
       }
       int s = 0;
@@ -265,23 +262,19 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
           mbar_await(&sh->v_full[s], ph, polls, ok);
           if (next) mbar_await(&sh->k_full[s1], ph1, polls, ok);
         }
+        mbar_await(&sh->p_full[m][u & 1], (uint32_t)((u >> 1) & 1), polls, ok);
+        tc_fence_after();
+        if (elect_one() && ok) {
+          const uint32_t vt = sbase + C::OFF_V + s * C::TILE + (u & 1) * 8192;
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          mbar_await(&sh->p_full[m][u & 1], (uint32_t)((u >> 1) & 1), polls, ok);
-          tc_fence_after();
-          if (elect_one() && ok) {
-            const uint32_t vt = sbase + C::OFF_V + s * C::TILE + (u & 1) * 8192;
-            const uint32_t pt = tmem + C::TM_S + 128 * m + 64 * (u & 1);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_bf16_ts(tmem + C::TM_O + 128 * m, pt + kk * 8, sw128_desc(vt + kk * 2048, 16384, 1024), C::IDESC_PV,
-                          (u > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(&sh->pv_done[m]);
-            if (m == 1 && ((u & 1) == 1 || u + 1 == steps)) mma_commit(&sh->v_empty[s]);
-            if (next) {
-              issue_s(m, u + 2, s1);  // over P, behind the product that reads it
-              if (m == 1 && ((u & 1) == 1 || u + 3 == steps)) mma_commit(&sh->k_empty[s1]);
-            }
+          for (int kk = 0; kk < 4; ++kk)
+            mma_bf16_ts(o_t, s_t + 64 * (u & 1) + kk * 8, sw128_desc(vt + kk * 2048, 16384, 1024), C::IDESC_PV,
+                        (u > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&sh->pv_done[m]);
+          if ((u & 1) == 1 || u + 1 == steps) mma_commit(&sh->v_empty[s]);
+          if (next) {
+            issue_s(u + 2, s1);  // over P, behind the product that reads it
+            if ((u & 1) == 1 || u + 3 == steps) mma_commit(&sh->k_empty[s1]);
           }
         }
         if (u & 1) {
