@@ -9,10 +9,10 @@
 // plain attention head of width d; the exponentials are doubled.
 //   diff_prep_kernel  D_1, D_2 and the log-sum-exps in base 2, rows padded to
 //                     whole tiles (pad rows: p = 0)
-//   diff_dq_kernel    one CTA per (query tile, b, h): S_1, S_2 and dP in tensor
-//                     memory, one thread a row and half of the keys; dS_1 and
-//                     dS_2 as bf16 over the dP columns that the thread has read;
-//                     and the CTA's share of dlam, in fp32 from p and dp themselves
+//   diff_dq_kernel    one CTA per (query tile, b, h), 64 keys a step in two buffers
+//                     of tensor memory: S_1, S_2 and dP, then dS_1 and dS_2 as bf16
+//                     over S_1; one thread a row and half of the step's keys; and
+//                     the CTA's share of dlam, in fp32 from p and dp themselves
 //   diff_dkdv_kernel  one CTA per (key tile, b, h) over the query tiles that keep
 //                     it, 64 queries a step: S_1^T, S_2^T and dP^T are read into
 //                     registers and replaced by the next step's at once; (P_1 -
@@ -43,7 +43,8 @@ struct DiffBwdShared {
   uint64_t fixed_full;
   uint64_t ring_full[4], ring_empty[4];                   // dK/dV kernel
   uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];  // dQ kernel
-  uint64_t s_full, dp_full, s_read, ds_full, mm_done;
+  uint64_t buf_full[2], buf_ds[2], buf_done[2];            // dQ kernel, per buffer
+  uint64_t s_full, s_read, ds_full, mm_done;               // dK/dV kernel
   uint64_t drain;
   uint32_t tmem_base;
   float part[8];  // dlam by warp
@@ -70,8 +71,7 @@ struct DiffBwdCfg {
   static constexpr int OFF_BAR = OFF_VEC + STAGES * VEC;
   static constexpr int USED = OFF_BAR + (int)sizeof(DiffBwdShared) + 1024;
   static constexpr int SMEM = USED > 122880 ? USED : 122880;
-  static constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false);
-  static constexpr uint32_t IDESC_SH = idesc_bf16(128, 64, false, false);  // 64 queries
+  static constexpr uint32_t IDESC_SH = idesc_bf16(128, 64, false, false);  // 64 keys or queries
   static constexpr uint32_t IDESC_H = idesc_bf16(128, 64, false, true);    // gradient of one half of q or k
   static constexpr uint32_t IDESC_V = idesc_bf16(128, D, false, true);
   static_assert(DQ_SMEM <= 232448 && SMEM <= 232448, "shared memory budget");
@@ -139,29 +139,6 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// s <- 2^(s c - l) for 32 scores of a row, 0 from column `valid` on.
-__device__ __forceinline__ void diff_exp32(uint32_t (&s)[32], uint64_t c2, uint64_t nl, int valid) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint64_t x = f32x2_fma(f32x2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), c2, nl);
-    float p0, p1;
-    if ((i & 3) == 3) {
-      exp2_fma_x2(x, p0, p1);
-    } else {
-      float x0, x1;
-      f32x2_unpack(x, x0, x1);
-      p0 = ex2_approx(x0);
-      p1 = ex2_approx(x1);
-    }
-    s[2 * i] = __float_as_uint(p0);
-    s[2 * i + 1] = __float_as_uint(p1);
-  }
-  if (valid < 32) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i >= valid) s[i] = 0u;
-  }
-}
 __device__ __forceinline__ uint64_t pair_of(const uint32_t (&s)[32], int i) {
   return f32x2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
 }
@@ -192,11 +169,13 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
                    uint16_t* __restrict__ dq, float* __restrict__ dlam_part, int N, int heads, int nb, int npad,
                    int mask_per_bh, float scale, float scale_log2, uint32_t* status, uint64_t limit_ns) {
   using C = DiffBwdCfg<D>;
-  // S_1 [0,128), S_2 [128,256), dP [256,384): a thread's half e of the keys is
-  // dP [256 + 64 e, +64), over which it writes dS_1 (32 columns) and dS_2 (32);
-  // dQ_1 [384,448), dQ_2 [448,512).  At d = 64 the two products take both halves
-  // of k (N = 64) and the half that does not belong is left aside.
-  constexpr uint32_t TM_S = 0, TM_DP = 256, TM_DQ = 384;
+  // A step is 64 keys.  Two buffers of 192 columns, each S_1 [0,64), S_2 [64,128) and
+  // dP [128,192) of a step; a thread's half e of the keys is columns [32 e, +32) of
+  // each, and it writes dS_1 as bf16 over [32 e, +16) and dS_2 over [32 e + 16, +16)
+  // once it holds all three in registers.  dQ_1 [384,448), dQ_2 [448,512).  At d = 64
+  // the two products take both halves of k (N = 64) and the half that does not
+  // belong is left aside.
+  constexpr uint32_t TM_BUF = 192, TM_DP = 128, TM_DQ = 384;
   extern __shared__ uint8_t diff_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(diff_smem_raw) + 1023) & ~uintptr_t(1023));
   DiffBwdShared* sh = reinterpret_cast<DiffBwdShared*>(smem + C::DQ_OFF_BAR);
@@ -209,16 +188,20 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
   const int c0 = warp_uniform(row_ptr[mrow]);
   const int n = warp_uniform(debug_row_ok(row_ptr, col_idx, mrow, mask_rows, nb, true, status) ? row_ptr[mrow + 1] - c0 : 0);
 
+  // steps of 64 keys; columns ascend, so only the last tile can be short
+  const int last = warp_uniform(n > 0 ? min(128, N - col_idx[c0 + n - 1] * 128) : 0);
+  const int steps = 2 * n - (n > 0 && last <= 64 ? 1 : 0);
+
   if (threadIdx.x == 0) {
     mbar_init(&sh->fixed_full, 1);
     for (int st = 0; st < 3; ++st) mbar_init(&sh->k_full[st], 1), mbar_init(&sh->k_empty[st], 1);
     for (int st = 0; st < 2; ++st) mbar_init(&sh->v_full[st], 1), mbar_init(&sh->v_empty[st], 1);
-    mbar_init(&sh->dp_full, 1);
-    mbar_init(&sh->s_full, 1);
-    mbar_init(&sh->s_read, 8);
-    mbar_init(&sh->ds_full, 8);
-    mbar_init(&sh->mm_done, 1);
-    mbar_init(&sh->drain, 2);
+    for (int f = 0; f < 2; ++f) {
+      mbar_init(&sh->buf_full[f], 2);  // the scores and dP
+      mbar_init(&sh->buf_ds[f], 8);
+      mbar_init(&sh->buf_done[f], 1);
+    }
+    mbar_init(&sh->drain, 3);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -259,76 +242,63 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       for (int i = (vl > 2 ? vl - 2 : 0); i < vl; ++i)
         mbar_wait(&sh->v_full[i & 1], (uint32_t)((i >> 1) & 1), kDiffBwdDrainNs);
     }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------- tcgen05 issuer of S: of the
-    // next tile as soon as the row warps hold S in registers
-    if (n > 0) {  // (the whole warp; one lane issues)
+  } else if (warp < 4) {
+    // ---------------------------------------------------------- tcgen05 issuers: S of both maps
+    // (warp 1) and dP (warp 2) of a step into the buffer that the gradient products
+    // of two steps before have read, the gradient products (warp 3)
+    if (n > 0) {  // (whole warps; one lane issues)
       bool ok = limit_ns != 0;
       mbar_await(&sh->fixed_full, 0, polls, ok);
-      int s = 0;
-      uint32_t ph = 0;  // K stage and its parity
-      for (int j = 0; j < n; ++j) {
-        mbar_await(&sh->k_full[s], ph, polls, ok);
-        if (j > 0) mbar_await(&sh->s_read, (uint32_t)((j - 1) & 1), polls, ok);
+      int ks = 0;
+      uint32_t kph = 0;  // K stage and its parity
+      for (int u = 0; u < steps; ++u) {
+        const int f = u & 1, vs = (u >> 1) & 1;
+        const uint32_t ph = (uint32_t)((u >> 1) & 1), buf = tmem + TM_BUF * f, rows64 = 8192u * f;
+        const bool last_use = f == 1 || u + 1 == steps;  // of the step's key tile
+        if (warp == 2)
+          mbar_await(&sh->v_full[vs], (uint32_t)((u >> 2) & 1), polls, ok);
+        else
+          mbar_await(&sh->k_full[ks], kph, polls, ok);
+        if (warp == 3)
+          mbar_await(&sh->buf_ds[f], ph, polls, ok);
+        else if (u >= 2)
+          mbar_await(&sh->buf_done[f], ph ^ 1, polls, ok);
         tc_fence_after();
-        if (elect_one() && ok) {
-          const uint32_t kt = sbase + C::DQ_OFF_K + s * C::TILE;
-          mma_steps<D / 32>(tmem + TM_S, q_s, kt, 0, C::IDESC_S);
-          mma_steps<D / 32>(tmem + TM_S + 128, q_s, kt, D / 32, C::IDESC_S);
-          mma_commit(&sh->s_full);
+        const uint32_t kt = sbase + C::DQ_OFF_K + ks * C::TILE + rows64;
+        if (warp == 1) {
+          if (elect_one() && ok) {
+            mma_steps<D / 32>(buf, q_s, kt, 0, C::IDESC_SH);
+            mma_steps<D / 32>(buf + 64, q_s, kt, D / 32, C::IDESC_SH);
+            mma_commit(&sh->buf_full[f]);
+          }
+        } else if (warp == 2) {
+          if (elect_one() && ok) {
+            mma_steps<D / 16>(buf + TM_DP, do_s, sbase + C::DQ_OFF_V + vs * C::TILE + rows64, 0, C::IDESC_SH);
+            mma_commit(&sh->buf_full[f]);
+            if (last_use) mma_commit(&sh->v_empty[vs]);
+          }
+        } else if (elect_one() && ok) {
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_ts(tmem + TM_DQ + 64 * m, buf + 32 * (kk >> 1) + 16 * m + 8 * (kk & 1),
+                          sw128_desc(kt + (C::DCH == 2 ? m * 16384 : 0) + kk * 2048, 16384, 1024), C::IDESC_H,
+                          (u > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&sh->buf_done[f]);
+          if (last_use) mma_commit(&sh->k_empty[ks]);  // (S of this step ended before the row warps formed dS)
         }
-        s = s == 2 ? 0 : s + 1;
-        ph = s == 0 ? ph ^ 1 : ph;
+        if (f == 1) {
+          ks = ks == 2 ? 0 : ks + 1;
+          kph = ks == 0 ? kph ^ 1 : kph;
+        }
       }
       if (!__all_sync(0xffffffffu, ok)) diff_bwd_timeout(status);
       // every product has ended before the tensor memory is given back, also when a row warp gave up
       if (elect_one()) mma_commit(&sh->drain);
       mbar_wait_warp(&sh->drain, 0, kDiffBwdDrainNs);
     }
-  } else if (warp == 2) {
-    // ---------------------------------------------------------- tcgen05 issuer of dP and dQ:
-    // dP of the next tile over dS, behind the products that read it
-    if (n > 0) {
-      auto issue_dp = [&](int j) {
-        mma_steps<D / 16>(tmem + TM_DP, do_s, sbase + C::DQ_OFF_V + (j & 1) * C::TILE, 0, C::IDESC_S);
-        mma_commit(&sh->dp_full);
-        mma_commit(&sh->v_empty[j & 1]);
-      };
-      bool ok = limit_ns != 0;
-      mbar_await(&sh->fixed_full, 0, polls, ok);
-      mbar_await(&sh->v_full[0], 0, polls, ok);
-      tc_fence_after();
-      if (elect_one() && ok) issue_dp(0);
-      int s = 0;
-      uint32_t ph = 0;
-      for (int j = 0; j < n; ++j) {
-        mbar_await(&sh->k_full[s], ph, polls, ok);
-        if (j + 1 < n) mbar_await(&sh->v_full[(j + 1) & 1], (uint32_t)(((j + 1) >> 1) & 1), polls, ok);
-        mbar_await(&sh->ds_full, (uint32_t)(j & 1), polls, ok);
-        tc_fence_after();
-        if (elect_one() && ok) {
-          const uint32_t kt = sbase + C::DQ_OFF_K + s * C::TILE;
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_bf16_ts(tmem + TM_DQ + 64 * m, tmem + TM_DP + 64 * (kk >> 2) + 32 * m + 8 * (kk & 3),
-                          sw128_desc(kt + (C::DCH == 2 ? m * 16384 : 0) + kk * 2048, 16384, 1024), C::IDESC_H,
-                          (j > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&sh->k_empty[s]);  // (S of this tile ended before the row warps formed dS)
-          if (j + 1 < n)
-            issue_dp(j + 1);
-          else
-            mma_commit(&sh->mm_done);
-        }
-        s = s == 2 ? 0 : s + 1;
-        ph = s == 0 ? ph ^ 1 : ph;
-      }
-      if (!__all_sync(0xffffffffu, ok)) diff_bwd_timeout(status);
-      if (elect_one()) mma_commit(&sh->drain);
-      mbar_wait_warp(&sh->drain, 0, kDiffBwdDrainNs);
-    }
-  } else if (warp >= 4) {
+  } else {
     // one thread a query row and half of the keys of every tile
     const int quarter = warp & 3, r = quarter * 32 + lane, half = (warp - 4) >> 2;
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -337,64 +307,54 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     const uint64_t c2 = f32x2_pack(scale_log2, scale_log2), nl1 = f32x2_pack(-l1, -l1), nl2 = f32x2_pack(-l2, -l2);
     const uint64_t nd1 = f32x2_pack(-D1, -D1), nd2 = f32x2_pack(-D2, -D2);
     uint64_t dl2 = 0;  // (0, 0)
-    const int last = warp_uniform(n > 0 ? N - col_idx[c0 + n - 1] * 128 : 0);  // (columns ascend: only the last tile can be short)
     bool ok = limit_ns != 0;
-    for (int j = 0; j < n; ++j) {
-      const int valid = (j + 1 == n ? last : 128) - 64 * half;  // real keys from this half's first on
-      mbar_await(&sh->s_full, (uint32_t)(j & 1), polls, ok);
+    for (int u = 0; u < steps; ++u) {
+      const int f = u & 1;
+      const uint32_t buf = lane_addr + TM_BUF * f + 32 * half;
+      mbar_await(&sh->buf_full[f], (uint32_t)((u >> 1) & 1), polls, ok);
       tc_fence_after();
-      // P_1, then P_2: S is released once both are in registers, so that S of the
-      // next tile runs beside P_2's exponentials
-      uint32_t p1[2][32], p2[2][32];
-      tmem_ld32(lane_addr + TM_S + 64 * half, p1[0]);
-      tmem_ld32(lane_addr + TM_S + 64 * half + 32, p1[1]);
+      uint32_t s1[32], s2[32], g[32];
+      tmem_ld32(buf, s1);
+      tmem_ld32(buf + 64, s2);
+      tmem_ld32(buf + TM_DP, g);
       tmem_ld_wait();
+      if (u + 1 == steps) {  // (only the last step can be short)
+        const int valid = last - 64 * f - 32 * half;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) diff_exp32(p1[c], c2, nl1, valid - 32 * c);
-      tmem_ld32(lane_addr + TM_S + 128 + 64 * half, p2[0]);
-      tmem_ld32(lane_addr + TM_S + 128 + 64 * half + 32, p2[1]);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(&sh->s_read);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) diff_exp32(p2[c], c2, nl2, valid - 32 * c);
-      mbar_await(&sh->dp_full, (uint32_t)(j & 1), polls, ok);
-      tc_fence_after();
-      // (both chunks of a thread's dP are read before dS takes their place: the
-      // first chunk's dS_1 lies over the first chunk, its dS_2 over the second)
-      uint32_t a[2][16];
-      {
-        uint32_t g[32];
-        tmem_ld32(lane_addr + TM_DP + 64 * half, g);
-        tmem_ld_wait();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint64_t gi = pair_of(g, i);
-          a[0][i] = pack_pair(f32x2_mul(pair_of(p1[0], i), f32x2_add(gi, nd1)));
-          a[1][i] = pack_pair(f32x2_mul(pair_of(p2[0], i), f32x2_add(gi, nd2)));
-          dl2 = f32x2_fma(pair_of(p2[0], i), gi, dl2);
-        }
-        tmem_ld32(lane_addr + TM_DP + 64 * half + 32, g);
-        tmem_ld_wait();
-        tmem_st16(lane_addr + TM_DP + 64 * half, a[0]);
-        tmem_st16(lane_addr + TM_DP + 64 * half + 32, a[1]);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint64_t gi = pair_of(g, i);
-          a[0][i] = pack_pair(f32x2_mul(pair_of(p1[1], i), f32x2_add(gi, nd1)));
-          a[1][i] = pack_pair(f32x2_mul(pair_of(p2[1], i), f32x2_add(gi, nd2)));
-          dl2 = f32x2_fma(pair_of(p2[1], i), gi, dl2);
-        }
-        tmem_st16(lane_addr + TM_DP + 64 * half + 16, a[0]);
-        tmem_st16(lane_addr + TM_DP + 64 * half + 48, a[1]);
+        for (int i = 0; i < 32; ++i)
+          if (i >= valid) s1[i] = s2[i] = __float_as_uint(-INFINITY);
       }
+      uint32_t a[16], z[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const uint64_t x1 = f32x2_fma(pair_of(s1, k), c2, nl1), x2 = f32x2_fma(pair_of(s2, k), c2, nl2);
+        float p0, p1, q0, q1;
+        if ((k & 3) == 3) {
+          exp2_fma_x2(x1, p0, p1);
+          exp2_fma_x2(x2, q0, q1);
+        } else {
+          float y0, y1;
+          f32x2_unpack(x1, y0, y1);
+          p0 = ex2_approx(y0);
+          p1 = ex2_approx(y1);
+          f32x2_unpack(x2, y0, y1);
+          q0 = ex2_approx(y0);
+          q1 = ex2_approx(y1);
+        }
+        const uint64_t p = f32x2_pack(p0, p1), q = f32x2_pack(q0, q1), gi = pair_of(g, k);
+        a[k] = pack_pair(f32x2_mul(p, f32x2_add(gi, nd1)));
+        z[k] = pack_pair(f32x2_mul(q, f32x2_add(gi, nd2)));
+        dl2 = f32x2_fma(q, gi, dl2);
+      }
+      tmem_st16(buf, a);
+      tmem_st16(buf + 16, z);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(&sh->ds_full);
+      if (lane == 0 && ok) mbar_arrive(&sh->buf_ds[f]);
     }
-    if (n > 0) mbar_await(&sh->mm_done, 0, polls, ok);  // the last gradient products
+    // the last gradient products (those of the step before them came first)
+    if (n > 0) mbar_await(&sh->buf_done[(steps - 1) & 1], (uint32_t)(((steps - 1) >> 1) & 1), polls, ok);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) {
       diff_bwd_timeout(status);
