@@ -43,7 +43,7 @@ struct DiffBwdShared {
   uint64_t fixed_full;
   uint64_t ring_full[4], ring_empty[4];                   // dK/dV kernel
   uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];  // dQ kernel
-  uint64_t buf_full[2], buf_ds[2], buf_done[2];            // dQ kernel, per buffer
+  uint64_t buf_full[2], buf_read[2], buf_ds[2], buf_done[2];  // dQ kernel, per buffer
   uint64_t s_full, s_read, ds_full, mm_done;               // dK/dV kernel
   uint64_t drain;
   uint32_t tmem_base;
@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     for (int st = 0; st < 3; ++st) mbar_init(&sh->k_full[st], 1), mbar_init(&sh->k_empty[st], 1);
     for (int st = 0; st < 2; ++st) mbar_init(&sh->v_full[st], 1), mbar_init(&sh->v_empty[st], 1);
     for (int f = 0; f < 2; ++f) {
-      mbar_init(&sh->buf_full[f], 2);  // the scores and dP
+      mbar_init(&sh->buf_full[f], 2);  // S_1, and S_2 with dP
+      mbar_init(&sh->buf_read[f], 8);
       mbar_init(&sh->buf_ds[f], 8);
       mbar_init(&sh->buf_done[f], 1);
     }
@@ -243,9 +244,10 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
         mbar_wait(&sh->v_full[i & 1], (uint32_t)((i >> 1) & 1), kDiffBwdDrainNs);
     }
   } else if (warp < 4) {
-    // ---------------------------------------------------------- tcgen05 issuers: S of both maps
-    // (warp 1) and dP (warp 2) of a step into the buffer that the gradient products
-    // of two steps before have read, the gradient products (warp 3)
+    // ---------------------------------------------------------- tcgen05 issuers: S_2 and dP of
+    // a step (warp 2) once the row warps hold those of two steps before in registers,
+    // S_1 (warp 1), whose columns dS took, once the gradient products (warp 3) have
+    // read that
     if (n > 0) {  // (whole warps; one lane issues)
       bool ok = limit_ns != 0;
       mbar_await(&sh->fixed_full, 0, polls, ok);
@@ -255,24 +257,22 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
         const int f = u & 1, vs = (u >> 1) & 1;
         const uint32_t ph = (uint32_t)((u >> 1) & 1), buf = tmem + TM_BUF * f, rows64 = 8192u * f;
         const bool last_use = f == 1 || u + 1 == steps;  // of the step's key tile
-        if (warp == 2)
-          mbar_await(&sh->v_full[vs], (uint32_t)((u >> 2) & 1), polls, ok);
-        else
-          mbar_await(&sh->k_full[ks], kph, polls, ok);
+        mbar_await(&sh->k_full[ks], kph, polls, ok);
+        if (warp == 2) mbar_await(&sh->v_full[vs], (uint32_t)((u >> 2) & 1), polls, ok);
         if (warp == 3)
           mbar_await(&sh->buf_ds[f], ph, polls, ok);
         else if (u >= 2)
-          mbar_await(&sh->buf_done[f], ph ^ 1, polls, ok);
+          mbar_await(warp == 1 ? &sh->buf_done[f] : &sh->buf_read[f], ph ^ 1, polls, ok);
         tc_fence_after();
         const uint32_t kt = sbase + C::DQ_OFF_K + ks * C::TILE + rows64;
         if (warp == 1) {
           if (elect_one() && ok) {
             mma_steps<D / 32>(buf, q_s, kt, 0, C::IDESC_SH);
-            mma_steps<D / 32>(buf + 64, q_s, kt, D / 32, C::IDESC_SH);
             mma_commit(&sh->buf_full[f]);
           }
         } else if (warp == 2) {
           if (elect_one() && ok) {
+            mma_steps<D / 32>(buf + 64, q_s, kt, D / 32, C::IDESC_SH);
             mma_steps<D / 16>(buf + TM_DP, do_s, sbase + C::DQ_OFF_V + vs * C::TILE + rows64, 0, C::IDESC_SH);
             mma_commit(&sh->buf_full[f]);
             if (last_use) mma_commit(&sh->v_empty[vs]);
@@ -318,6 +318,9 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       tmem_ld32(buf + 64, s2);
       tmem_ld32(buf + TM_DP, g);
       tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(&sh->buf_read[f]);
       if (u + 1 == steps) {  // (only the last step can be short)
         const int valid = last - 64 * f - 32 * half;
 #pragma unroll
