@@ -630,9 +630,9 @@ int salad_diff_backward(const void* q, const void* k, const void* v, const void*
  *   q, out   DEVICE bf16 [B][Nq][Hh][d];  k, v  DEVICE bf16 [B][capacity][Hh][d]; 16-byte aligned.
  *   lens     DEVICE int32 [B], taken as 0 below 0 and as capacity above it; 0: out is 0.
  *            Keys and values from lens[b] on are not read.
- * fp32 arithmetic, one rounding, a fixed order of sums; no workspace.  Meant for
- * Nq of about four or fewer (the keys are read once per four queries).  Errors:
- * INVALID_ARG, UNSUPPORTED (d, B*Hh*16 >= 2^31, Nq > 262140), CUDA.
+ * fp32 arithmetic, one rounding, a fixed order of sums; no workspace.  Meant
+ * for one or two queries (the keys are read once per pair of them).  Errors:
+ * INVALID_ARG, UNSUPPORTED (d, B*Hh*16 >= 2^31, Nq > 131070), CUDA.
  */
 int salad_diff_decode(const void* q, const void* k, const void* v, int B, int Nq, int capacity, int num_heads, int d,
                       const int32_t* lens, const void* lam, int lam_type, float softmax_scale, void* out,

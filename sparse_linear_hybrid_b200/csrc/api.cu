@@ -1217,7 +1217,7 @@ int salad_diff_decode(const void* q, const void* k, const void* v, int B, int Nq
       !aligned(lam, type_bytes(lam_type)) || !std::isfinite(softmax_scale))
     return SALAD_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return SALAD_ERR_UNSUPPORTED;
-  if ((long long)B * num_heads >= (1ll << 31) / 16 || Nq > 262140 || capacity > (1 << 30)) return SALAD_ERR_UNSUPPORTED;
+  if ((long long)B * num_heads >= (1ll << 31) / 16 || Nq > 131070 || capacity > (1 << 30)) return SALAD_ERR_UNSUPPORTED;
   const size_t row = (size_t)num_heads * d * 2, qb = (size_t)B * Nq * row, kb = (size_t)B * capacity * row;
   if (overlaps(out, qb, q, qb) || overlaps(out, qb, k, kb) || overlaps(out, qb, v, kb)) return SALAD_ERR_INVALID_ARG;
   DiffDecodeArgs a{};

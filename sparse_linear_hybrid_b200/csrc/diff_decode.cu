@@ -1,9 +1,9 @@
-// Differential attention (diff.cu) of a few query rows, one to four in general,
-// against a cache of keys and values: query i of sequence b sees keys [0, lens[b])
-// (0 keys: the output is 0).
+// Differential attention (diff.cu) of a few query rows, one in general, against a
+// cache of keys and values: query i of sequence b sees keys [0, lens[b]) (0 keys:
+// the output is 0).
 //
-// Bound by memory: each live key and value is read once per group of up to four
-// queries.  The keys of a (b, h) are split over the CTAs of a cluster (up to 16)
+// Bound by memory: each live key and value is read once per query or pair of
+// queries (4 x 32,760 keys x 12 heads of 128, one query each: 138 us, 5.84 TB/s).  The keys of a (b, h) are split over the CTAs of a cluster (up to 16)
 // so that a short batch still fills the machine; every warp keeps an online
 // softmax of its keys (running maxima, sums and weighted values of both maps in
 // fp32 registers, d/8 lanes a key, eight features a lane), the warps join in
@@ -23,7 +23,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kDecWarps = 8;
-constexpr int kDecDeep = 4;  // keys in flight a lane group
+constexpr int kDecSplits = 16;
 
 // Joins (m, l, acc) of another part into this one.
 template <int E>
@@ -45,14 +45,24 @@ __device__ __forceinline__ void widen8(const uint4& r, float (&v)[8]) {
   }
 }
 
+// CTAs an SM, and keys a lane group works on at once (as many again are on their
+// way): what keeps the registers within bounds without spills.
+template <int NQ>
+struct DecCfg {
+  static constexpr int CTAS = 2;
+  static constexpr int DEEP = NQ == 1 ? 3 : 1;
+};
+
 template <int D, int NQ>
-__global__ void __launch_bounds__(32 * kDecWarps)
+__global__ void __launch_bounds__(32 * kDecWarps, DecCfg<NQ>::CTAS)
     diff_decode_kernel(const DiffDecodeArgs a, int splits) {
   constexpr int LPK = D / 8;          // lanes a key
   constexpr int KPW = 32 / LPK;       // keys a warp takes at once
-  // per query and map: maximum, sum, weighted values of the warps, then of the CTA
+  constexpr int DEEP = DecCfg<NQ>::DEEP;
+  // per query and map: maximum, sum and weighted values of the warps, then of the CTA
   __shared__ float sm[NQ][2][kDecWarps], sl[NQ][2][kDecWarps];
   __shared__ __align__(16) float sacc[NQ][2][kDecWarps][D];
+  __shared__ float cm[NQ][2], cl[NQ][2], cacc[NQ][2][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = blockIdx.x % splits, bh = blockIdx.x / splits, b = bh / a.heads, h = bh % a.heads;
   const int q0 = blockIdx.y * NQ;
@@ -84,24 +94,30 @@ __global__ void __launch_bounds__(32 * kDecWarps)
   const uint16_t* kp = a.k + (int64_t)b * a.cap * row + (int64_t)h * D + part * 8;
   const uint16_t* vp = a.v + (int64_t)b * a.cap * row + (int64_t)h * D + part * 8;
   const bool first = part < LPK / 2;
-  for (int base = k0 + warp * KPW; base < k1; base += kDecWarps * KPW * kDecDeep) {  // (the same in all lanes)
-    uint4 kr[kDecDeep], vr[kDecDeep];
-    bool live[kDecDeep];
+  constexpr int STEP = kDecWarps * KPW * DEEP;  // keys of the CTA an iteration
+  auto fetch = [&](int base, uint4 (&kr)[DEEP], uint4 (&vr)[DEEP]) {
 #pragma unroll
-    for (int u = 0; u < kDecDeep; ++u) {
+    for (int u = 0; u < DEEP; ++u) {
       const int key = base + u * kDecWarps * KPW + slot;
-      live[u] = key < k1;
       kr[u] = vr[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (live[u]) {
+      if (key < k1) {
         kr[u] = __ldcs(reinterpret_cast<const uint4*>(kp + key * row));
         vr[u] = __ldcs(reinterpret_cast<const uint4*>(vp + key * row));
       }
     }
+  };
+  // the next iteration's keys and values are on their way while one is worked on
+  uint4 kr[2][DEEP], vr[2][DEEP];
+  fetch(k0 + warp * KPW, kr[0], vr[0]);
+  auto work = [&](int base, const uint4 (&kr)[DEEP], const uint4 (&vr)[DEEP]) {
+    bool live[DEEP];
+#pragma unroll
+    for (int u = 0; u < DEEP; ++u) live[u] = base + u * kDecWarps * KPW + slot < k1;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      float s1[kDecDeep], s2[kDecDeep], t1 = m1[i], t2 = m2[i];
+      float s1[DEEP], s2[DEEP], t1 = m1[i], t2 = m2[i];
 #pragma unroll
-      for (int u = 0; u < kDecDeep; ++u) {
+      for (int u = 0; u < DEEP; ++u) {
         float k8[8], s = 0.f;
         widen8(kr[u], k8);
 #pragma unroll
@@ -121,7 +137,7 @@ __global__ void __launch_bounds__(32 * kDecWarps)
 #pragma unroll
       for (int f = 0; f < 8; ++f) acc1[i][f] *= g1, acc2[i][f] *= g2;
 #pragma unroll
-      for (int u = 0; u < kDecDeep; ++u) {
+      for (int u = 0; u < DEEP; ++u) {
         const float p1 = live[u] ? ex2_approx(s1[u] - t1) : 0.f, p2 = live[u] ? ex2_approx(s2[u] - t2) : 0.f;
         float v8[8];
         widen8(vr[u], v8);
@@ -136,6 +152,12 @@ __global__ void __launch_bounds__(32 * kDecWarps)
       m1[i] = t1;
       m2[i] = t2;
     }
+  };
+  for (int base = k0 + warp * KPW; base < k1; base += 2 * STEP) {  // (the same in all lanes)
+    fetch(base + STEP, kr[1], vr[1]);
+    work(base, kr[0], vr[0]);
+    fetch(base + 2 * STEP, kr[0], vr[0]);
+    work(base + STEP, kr[1], vr[1]);
   }
   // the key slots of a warp, then the warps
 #pragma unroll
@@ -162,31 +184,54 @@ __global__ void __launch_bounds__(32 * kDecWarps)
     }
     if (lane == 0) sm[i][0][warp] = m1[i], sl[i][0][warp] = l1[i], sm[i][1][warp] = m2[i], sl[i][1][warp] = l2[i];
   }
+  __syncthreads();
+  // the warps of this CTA: one thread a query, map and feature
+  for (int t = threadIdx.x; t < NQ * 2 * D; t += 32 * kDecWarps) {
+    const int i = t / (2 * D), x = t / D % 2, f = t % D;
+    float m = -INFINITY, l = 0.f, acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) m = fmaxf(m, sm[i][x][w]);
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+      const float g = sm[i][x][w] == -INFINITY ? 0.f : ex2_approx(sm[i][x][w] - m);
+      l += g * sl[i][x][w];
+      acc += g * sacc[i][x][w][f];
+    }
+    cacc[i][x][f] = acc;
+    if (f == 0) cm[i][x] = m, cl[i][x] = l;
+  }
   cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
-  // The warps of every CTA of the cluster, one thread an output feature: CTA c
-  // takes the features f with f % splits == c.
+  // The CTAs of the cluster: CTA c finishes every splits-th value from c on.  All
+  // loads of a value are on their way before the first is used.
   const float lam = a.lam_bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.lam)[h] << 16)
                                : static_cast<const float*>(a.lam)[h];
-  const int mine = D / splits;  // (splits <= 16 divides d)
-  for (int t = threadIdx.x; t < NQ * mine; t += 32 * kDecWarps) {
-    const int i = t / mine, f = split * mine + t % mine;
+  for (int t = split + splits * threadIdx.x; t < NQ * D; t += splits * 32 * kDecWarps) {
+    const int i = t / D, f = t % D;
     if (q0 + i >= a.Nq) continue;
     float o[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      float m = -INFINITY, l = 0.f, acc[1] = {0.f};
-      for (int c = 0; c < splits; ++c) {
-        const float* pm = cluster.map_shared_rank(&sm[i][x][0], c);
-        const float* pl = cluster.map_shared_rank(&sl[i][x][0], c);
-        const float* pa = cluster.map_shared_rank(&sacc[i][x][0][f], c);
+      float pm[kDecSplits], pl[kDecSplits], pa[kDecSplits];
 #pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) {
-          const float one[1] = {pa[w * D]};
-          join(m, l, acc, pm[w], pl[w], one);
+      for (int c = 0; c < kDecSplits; ++c) {
+        pm[c] = -INFINITY, pl[c] = 0.f, pa[c] = 0.f;
+        if (c < splits) {
+          pm[c] = *cluster.map_shared_rank(&cm[i][x], c);
+          pl[c] = *cluster.map_shared_rank(&cl[i][x], c);
+          pa[c] = *cluster.map_shared_rank(&cacc[i][x][f], c);
         }
       }
-      o[x] = len > 0 ? acc[0] / l : 0.f;
+      float m = -INFINITY, l = 0.f, acc = 0.f;
+#pragma unroll
+      for (int c = 0; c < kDecSplits; ++c) m = fmaxf(m, pm[c]);
+#pragma unroll
+      for (int c = 0; c < kDecSplits; ++c) {
+        const float g = pm[c] == -INFINITY ? 0.f : ex2_approx(pm[c] - m);
+        l += g * pl[c];
+        acc += g * pa[c];
+      }
+      o[x] = len > 0 ? acc / l : 0.f;
     }
     const uint32_t y = pack_bf16x2(fmaf(-lam, o[1], o[0]), 0.f);
     a.out[(((int64_t)b * a.Nq + q0 + i) * a.heads + h) * D + f] = (uint16_t)(y & 0xFFFFu);
@@ -194,12 +239,22 @@ __global__ void __launch_bounds__(32 * kDecWarps)
   cluster.sync();  // a CTA's shared memory outlives its last reader
 }
 
+// Splits of a (b, h)'s keys.  The CTAs fill the machine once, and clusters only
+// nine tenths of it: they do not fit into what other clusters leave of a GPC, and a
+// second wave costs as much as the first (48 units: 5 splits 138 us, 6 splits 201).
+// Where that would leave more than a quarter of the machine idle, many small CTAs
+// in several waves (192 units: 1 split 161 us, 4 splits 142).  256 keys a CTA at
+// least, 16 CTAs a cluster at most.
+template <int NQ>
+int decode_splits(int64_t units, int cap) {
+  const int64_t once = 134 * DecCfg<NQ>::CTAS / units;
+  const int64_t want = once >= 3 ? once : (370 * DecCfg<NQ>::CTAS + units - 1) / units;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, ((int64_t)cap + 255) / 256, kDecSplits}));
+}
+
 template <int D, int NQ>
 cudaError_t launch_diff_decode_t(const DiffDecodeArgs& a, cudaStream_t s) {
-  // Enough CTAs for two an SM, at least 64 keys each, at most 16 in a cluster.
-  const int64_t units = (int64_t)a.B * a.heads * ((a.Nq + NQ - 1) / NQ);
-  int splits = 1;
-  while (splits < 16 && units * splits < 296 && (int64_t)a.cap > 64 * splits) splits *= 2;
+  const int splits = decode_splits<NQ>((int64_t)a.B * a.heads * ((a.Nq + NQ - 1) / NQ), a.cap);
   if (splits > 8) {
     const cudaError_t e =
         cudaFuncSetAttribute(diff_decode_kernel<D, NQ>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -221,8 +276,7 @@ cudaError_t launch_diff_decode_t(const DiffDecodeArgs& a, cudaStream_t s) {
 template <int D>
 cudaError_t launch_diff_decode_d(const DiffDecodeArgs& a, cudaStream_t s) {
   if (a.Nq == 1) return launch_diff_decode_t<D, 1>(a, s);
-  if (a.Nq == 2) return launch_diff_decode_t<D, 2>(a, s);
-  return launch_diff_decode_t<D, 4>(a, s);
+  return launch_diff_decode_t<D, 2>(a, s);
 }
 
 }  // namespace
