@@ -171,7 +171,7 @@ def _check(status: int, what: str) -> None:
 
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:  # (the current stream's handle without a Stream object around it)
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -543,19 +543,31 @@ def _on(*tensors):
     """(context that makes the tensors' device current, that device); all have to be on one CUDA device."""
     dev = None
     for t in tensors:
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError("the tensors must be CUDA tensors (libsalad has no CPU path)")
-        d = t.get_device()
-        if dev is None:
+        try:
+            d = t.get_device()  # (-1: not a CUDA tensor)
+        except AttributeError:
+            d = -1
+        if d != dev:
+            if d < 0:
+                raise TypeError("the tensors must be CUDA tensors (libsalad has no CPU path)")
+            if dev is not None:
+                raise ValueError(f"the tensors lie on several devices: cuda:{dev} and cuda:{d}")
             dev = d
-        elif d != dev:
-            raise ValueError(f"the tensors lie on several devices: cuda:{dev} and cuda:{d}")
-    return (_NULL if dev == torch.cuda.current_device() else torch.cuda.device(dev)), tensors[0].device
+    return (_NULL if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)), tensors[0].device
+
+
+def _ptr(t, dtype, name) -> int:
+    """_dev_ptr's checks for a tensor that _on has seen; the bare address."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _new_like(x, dtype):
     """Contiguous memory of x's shape."""
-    return torch.empty_like(x) if x.dtype == dtype and x.is_contiguous() else x.new_empty(x.shape, dtype=dtype)
+    return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
 
 
 def rope_inv_freq(rot: int, base: float = 10000.0, sections=None, scaling: str | None = None, factor: float = 1.0,
@@ -757,12 +769,13 @@ def ckpt_pack(x, fmt: str = "int8", out=None, stream=None):
                 raise TypeError("tensors of fp32, bf16 or fp16 with one dimension at least")
             scales = _ckpt_scales_shape(t.shape)
             if c is None:
-                c = Checkpoint(t.new_empty(t.shape, dtype=torch.uint8), t.new_empty(scales, dtype=torch.uint8), fmt, t.dtype)
+                codes = torch.empty_like(t, dtype=torch.uint8, memory_format=torch.contiguous_format)
+                c = Checkpoint(codes, codes.new_empty(scales), fmt, t.dtype)
             else:
                 if c.codes.shape != t.shape or c.scales.shape != scales:
                     raise ValueError("the checkpoint's memory has another shape")
                 _on(t, c.codes, c.scales)
-                _dev_ptr(c.codes, torch.uint8, "codes"), _dev_ptr(c.scales, torch.uint8, "scales")
+                _ptr(c.codes, torch.uint8, "codes"), _ptr(c.scales, torch.uint8, "scales")
                 c.fmt, c.dtype = fmt, t.dtype
             res.append(c)
         _ckpt_call(lib().salad_ckpt_pack, "salad_ckpt_pack", xs, res, fmt, stream)
@@ -784,11 +797,11 @@ def ckpt_unpack(ckpt, dtype=None, out=None, stream=None):
     res = []
     with ctx:
         for c, y in zip(cks, outs):
-            _dev_ptr(c.codes, torch.uint8, "codes"), _dev_ptr(c.scales, torch.uint8, "scales")
+            _ptr(c.codes, torch.uint8, "codes"), _ptr(c.scales, torch.uint8, "scales")
             if c.scales.shape != _ckpt_scales_shape(c.codes.shape):
                 raise ValueError("scales and codes have shapes that do not agree")
             if y is None:
-                y = c.codes.new_empty(c.codes.shape, dtype=dtype or c.dtype)
+                y = torch.empty_like(c.codes, dtype=dtype or c.dtype)
             else:
                 _on(c.codes, y)
             if y.shape != c.codes.shape:
@@ -860,10 +873,11 @@ def new_diff_workspace(B: int, N: int, heads: int, d: int, device=None) -> torch
 
 
 def _bf16_like(q, *named):
+    shape = q.shape
     for t, name in named:
-        if t.shape != q.shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(q.shape)}")
-    return [_dev_ptr(t, torch.bfloat16, name) for t, name in named]
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    return [_ptr(t, torch.bfloat16, name) for t, name in named]
 
 
 def _lam(lam, heads):
@@ -871,13 +885,12 @@ def _lam(lam, heads):
         raise ValueError(f"lam has shape {tuple(lam.shape)}, not ({heads},)")
     if lam.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"lam must be fp32 or bf16, got {lam.dtype}")
-    return _dev_ptr(lam, lam.dtype, "lam"), _TYPES[lam.dtype]
+    return _ptr(lam, lam.dtype, "lam"), _TYPES[lam.dtype]
 
 
 def _cols(col_idx, row_ptr):
     """The column list's pointer; a mask that keeps nothing has none, and none is read."""
-    p = _dev_ptr(col_idx, torch.int32, "col_idx")
-    return p if col_idx.numel() else _dev_ptr(row_ptr, torch.int32, "row_ptr")
+    return _ptr(col_idx, torch.int32, "col_idx") or _ptr(row_ptr, torch.int32, "row_ptr")
 
 
 def _mask_rows(row_ptr, B, N, heads, mask_per_bh):
@@ -887,7 +900,7 @@ def _mask_rows(row_ptr, B, N, heads, mask_per_bh):
 
 
 def _diff_forward(q, k, v, row_ptr, col_idx, lam, softmax_scale, mask_per_bh, out, out2, lse, train, workspace, stream):
-    ctx, dev = _on(q, k, v, row_ptr, col_idx, lam)
+    ctx, dev = _on(q, k, v, row_ptr, col_idx, lam, *(t for t in (out, out2, lse, workspace) if t is not None))
     with ctx:
         B, N, Hh, d = q.shape
         _mask_rows(row_ptr, B, N, Hh, mask_per_bh)
@@ -900,12 +913,11 @@ def _diff_forward(q, k, v, row_ptr, col_idx, lam, softmax_scale, mask_per_bh, ou
                 raise ValueError(f"lse has shape {tuple(lse.shape)}, not {(2, B, Hh, N)}")
         if workspace is None:
             workspace = new_diff_workspace(B, N, Hh, d, dev)
-        _on(q, out, workspace, *([out2, lse] if train else []))
         ptrs = _bf16_like(q, (q, "q"), (k, "k"), (v, "v"), (out, "out"), *([(out2, "out2")] if train else []))
         _check(lib().salad_diff_forward(
-            *ptrs[:3], B, N, Hh, d, 128, _dev_ptr(row_ptr, torch.int32, "row_ptr"), _cols(col_idx, row_ptr), int(bool(mask_per_bh)), *_lam(lam, Hh), float(softmax_scale),
-            ptrs[3], ptrs[4] if train else None, _dev_ptr(lse, torch.float32, "lse") if train else None,
-            _dev_ptr(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)), "salad_diff_forward")
+            *ptrs[:3], B, N, Hh, d, 128, _ptr(row_ptr, torch.int32, "row_ptr"), _cols(col_idx, row_ptr), int(bool(mask_per_bh)), *_lam(lam, Hh), float(softmax_scale),
+            ptrs[3], ptrs[4] if train else None, _ptr(lse, torch.float32, "lse") if train else None,
+            _ptr(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)), "salad_diff_forward")
     return out, out2, lse
 
 
@@ -934,7 +946,8 @@ def diff_attn_backward(q, k, v, out, out2, dout, lse, row_ptr, col_idx, lam, t_r
     """Gradients of differential attention (see salad_diff_backward): dict of dq, dk,
     dv bf16 [B, N, Hh, d] and dlam [Hh] of lam's type.  out, out2 and lse come from
     diff_attn_forward_lse on the same inputs; the transposed mask as in attn_backward_sparse."""
-    ctx, dev = _on(q, k, v, out, out2, dout, lse, row_ptr, col_idx, lam)
+    ctx, dev = _on(q, k, v, out, out2, dout, lse, row_ptr, col_idx, lam,
+                   *(t for t in (t_row_ptr, t_col_idx, workspace) if t is not None))
     with ctx:
         B, N, Hh, d = q.shape
         _mask_rows(row_ptr, B, N, Hh, mask_per_bh)
@@ -947,14 +960,13 @@ def diff_attn_backward(q, k, v, out, out2, dout, lse, row_ptr, col_idx, lam, t_r
         res["dlam"] = torch.empty_like(lam)
         if workspace is None:
             workspace = new_diff_workspace(B, N, Hh, d, dev)
-        _on(q, t_row_ptr, t_col_idx, workspace)
         ptrs = _bf16_like(q, (q, "q"), (k, "k"), (v, "v"), (out, "out"), (out2, "out2"), (dout, "dout"))
-        i32 = lambda t, name: _dev_ptr(t, torch.int32, name)  # noqa: E731
+        i32 = lambda t, name: _ptr(t, torch.int32, name)  # noqa: E731
         _check(lib().salad_diff_backward(
-            *ptrs, _dev_ptr(lse, torch.float32, "lse"), B, N, Hh, d, 128, i32(row_ptr, "row_ptr"),
+            *ptrs, _ptr(lse, torch.float32, "lse"), B, N, Hh, d, 128, i32(row_ptr, "row_ptr"),
             _cols(col_idx, row_ptr), i32(t_row_ptr, "t_row_ptr"), _cols(t_col_idx, t_row_ptr), int(bool(mask_per_bh)),
-            *_lam(lam, Hh), float(softmax_scale), *[_dev_ptr(res[n], torch.bfloat16, n) for n in ("dq", "dk", "dv")],
-            ctypes.c_void_p(res["dlam"].data_ptr()), _dev_ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
+            *_lam(lam, Hh), float(softmax_scale), *[_ptr(res[n], torch.bfloat16, n) for n in ("dq", "dk", "dv")],
+            res["dlam"].data_ptr(), _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
             _stream(stream)), "salad_diff_backward")
     return res
 
@@ -963,7 +975,7 @@ def diff_attn_decode(q, k_cache, v_cache, lens, lam, softmax_scale: float = 0.0,
     """Differential attention of a few queries against a cache (see salad_diff_decode):
     q bf16 [B, Nq, Hh, d], k_cache and v_cache bf16 [B, capacity, Hh, d], lens int32
     CUDA [B]; every query of sequence b sees keys [0, lens[b])."""
-    ctx, _ = _on(q, k_cache, v_cache, lens, lam)
+    ctx, _ = _on(q, k_cache, v_cache, lens, lam, *(() if out is None else (out,)))
     with ctx:
         B, Nq, Hh, d = q.shape
         cap = k_cache.shape[1]
@@ -971,11 +983,10 @@ def diff_attn_decode(q, k_cache, v_cache, lens, lam, softmax_scale: float = 0.0,
             raise ValueError("k_cache, v_cache [B, capacity, Hh, d] and lens [B] must fit q")
         if out is None:
             out = torch.empty_like(q)
-        _on(q, out)
         ptrs = _bf16_like(q, (q, "q"), (out, "out"))
         _check(lib().salad_diff_decode(
-            ptrs[0], _dev_ptr(k_cache, torch.bfloat16, "k_cache"), _dev_ptr(v_cache, torch.bfloat16, "v_cache"), B, Nq,
-            cap, Hh, d, _dev_ptr(lens, torch.int32, "lens"), *_lam(lam, Hh), float(softmax_scale), ptrs[1],
+            ptrs[0], _ptr(k_cache, torch.bfloat16, "k_cache"), _ptr(v_cache, torch.bfloat16, "v_cache"), B, Nq,
+            cap, Hh, d, _ptr(lens, torch.int32, "lens"), *_lam(lam, Hh), float(softmax_scale), ptrs[1],
             _stream(stream)), "salad_diff_decode")
     return out
 

@@ -1146,13 +1146,13 @@ int salad_diff_forward(const void* q, const void* k, const void* v, int B, int N
   CUtensorMap tq, tk, tv, to, to2;
   if (!make_head_map(&tq, q, B, N, num_heads, d, 128) || !make_head_map(&tk, k, B, N, num_heads, d, 128) ||
       !make_head_map(&tv, v, B, N, num_heads, d, 128) || !make_head_map(&to, out, B, N, num_heads, d, 128) ||
-      !make_head_map(&to2, out2 ? out2 : out, B, N, num_heads, d, 128))
+      (out2 && !make_head_map(&to2, out2, B, N, num_heads, d, 128)))
     return SALAD_ERR_CUDA;
   a.tm_q = &tq;
   a.tm_k = &tk;
   a.tm_v = &tv;
   a.tm_out = &to;
-  a.tm_out2 = &to2;
+  a.tm_out2 = out2 ? &to2 : &to;
   a.lse = lse;
   return launch_diff_forward(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SALAD_OK : SALAD_ERR_CUDA;
 }
