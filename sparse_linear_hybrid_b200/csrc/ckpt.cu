@@ -7,9 +7,10 @@
 // at most 7 (int8) or 4 (e4m3) significant bits: exact in bf16.  A group that
 // holds an infinity or a NaN has the byte 255 and decodes to NaN.
 //
-// Bound by memory: 2 + 1 + 1/32 bytes a bf16 value each way.  A lane takes 16
-// values (two 16-byte loads of bf16, one 16-byte store of codes), two lanes a
-// group, two such pieces in flight a lane.  Rounding to int8 adds 1.5 2^23 (the
+// Bound by memory: 2 + 1 + 1/32 bytes a bf16 value each way (three tensors of 50 M
+// values packed and unpacked again: 148 us, 6.2 TB/s).  A lane takes 16 values (two
+// 16-byte loads of bf16, one 16-byte store of codes), two lanes a group; more
+// pieces a lane were slower (two 153 us, four 157).  Rounding to int8 adds 1.5 2^23 (the
 // fused multiply-add rounds to an integer that sits in the low byte), so no
 // conversion instruction is needed on that side.
 #include <cuda_bf16.h>
@@ -22,7 +23,6 @@ namespace salad {
 namespace {
 
 constexpr int kCkptThreads = 256;
-constexpr int kCkptPieces = 2;  // 16-value pieces a lane
 constexpr float kRound = 12582912.f;  // 1.5 * 2^23
 
 __device__ __forceinline__ float f32_of(float x) { return x; }
@@ -173,38 +173,26 @@ __global__ void __launch_bounds__(kCkptThreads) ckpt_pack_kernel(const CkptArgs 
   const CkptPart& p = a.part[blockIdx.y];
   const T* x = static_cast<const T*>(p.x);
   const uint32_t per_row = (uint32_t)(a.cols / 16), total = (uint32_t)a.rows * per_row;
-  const uint32_t first = blockIdx.x * (kCkptThreads * kCkptPieces) + threadIdx.x;
-  uint4 raw[kCkptPieces][sizeof(T)];
+  const uint32_t id = blockIdx.x * kCkptThreads + threadIdx.x;
+  float v[16];
+  uint32_t top = 0;
+  if (id < total) {
+    uint4 raw[sizeof(T)];
+    const uint32_t row = a.one_row ? 0u : id / per_row;
+    load16(x + (int64_t)row * p.stride + (int64_t)(id - row * per_row) * 16, raw);
+    widen(raw, v, T{});
 #pragma unroll
-  for (int k = 0; k < kCkptPieces; ++k) {
-    const uint32_t id = first + k * kCkptThreads;
-    if (id < total) {
-      const uint32_t row = a.one_row ? 0u : id / per_row;
-      load16(x + (int64_t)row * p.stride + (int64_t)(id - row * per_row) * 16, raw[k]);
-    }
+    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
   }
-#pragma unroll
-  for (int k = 0; k < kCkptPieces; ++k) {
-    const uint32_t id = first + k * kCkptThreads;
-    float v[16];
-    uint32_t top = 0;
-    if (id < total) {
-      widen(raw[k], v, T{});
-#pragma unroll
-      for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    }
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    if (id < total) {
-      const int byte = scale_byte<FP8>(top);
-      const float inv = inverse_scale(byte);
-      uint4 c = make_uint4(0u, 0u, 0u, 0u);
-      if (byte != 255)
-        c = make_uint4(encode4<FP8>(v, inv), encode4<FP8>(v + 4, inv), encode4<FP8>(v + 8, inv),
-                       encode4<FP8>(v + 12, inv));
-      __stcs(reinterpret_cast<uint4*>(p.codes) + id, c);
-      if ((threadIdx.x & 1) == 0) p.scales[id / 2] = (uint8_t)byte;
-    }
-  }
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  if (id >= total) return;
+  const int byte = scale_byte<FP8>(top);
+  const float inv = inverse_scale(byte);
+  uint4 c = make_uint4(0u, 0u, 0u, 0u);
+  if (byte != 255)
+    c = make_uint4(encode4<FP8>(v, inv), encode4<FP8>(v + 4, inv), encode4<FP8>(v + 8, inv), encode4<FP8>(v + 12, inv));
+  __stcs(reinterpret_cast<uint4*>(p.codes) + id, c);
+  if ((threadIdx.x & 1) == 0) p.scales[id / 2] = (uint8_t)byte;
 }
 
 template <typename T, bool FP8>
@@ -212,34 +200,22 @@ __global__ void __launch_bounds__(kCkptThreads) ckpt_unpack_kernel(const CkptArg
   const CkptPart& p = a.part[blockIdx.y];
   T* y = static_cast<T*>(p.y);
   const uint32_t per_row = (uint32_t)(a.cols / 16), total = (uint32_t)a.rows * per_row;
-  const uint32_t first = blockIdx.x * (kCkptThreads * kCkptPieces) + threadIdx.x;
-  uint4 c[kCkptPieces];
-  int byte[kCkptPieces];
+  const uint32_t id = blockIdx.x * kCkptThreads + threadIdx.x;
+  if (id >= total) return;
+  const uint4 c = __ldcs(reinterpret_cast<const uint4*>(p.codes) + id);
+  const int byte = p.scales[id / 2];
+  const float scale = scale_of(byte);
+  float v[16];
+  decode4<FP8>(c.x, scale, v);
+  decode4<FP8>(c.y, scale, v + 4);
+  decode4<FP8>(c.z, scale, v + 8);
+  decode4<FP8>(c.w, scale, v + 12);
+  if (byte >= Top<T>::byte) {
 #pragma unroll
-  for (int k = 0; k < kCkptPieces; ++k) {
-    const uint32_t id = first + k * kCkptThreads;
-    if (id < total) {
-      c[k] = __ldcs(reinterpret_cast<const uint4*>(p.codes) + id);
-      byte[k] = p.scales[id / 2];
-    }
+    for (int i = 0; i < 16; ++i) v[i] = capped<T>(v[i], byte);
   }
-#pragma unroll
-  for (int k = 0; k < kCkptPieces; ++k) {
-    const uint32_t id = first + k * kCkptThreads;
-    if (id >= total) break;
-    float v[16];
-    const float scale = scale_of(byte[k]);
-    decode4<FP8>(c[k].x, scale, v);
-    decode4<FP8>(c[k].y, scale, v + 4);
-    decode4<FP8>(c[k].z, scale, v + 8);
-    decode4<FP8>(c[k].w, scale, v + 12);
-    if (byte[k] >= Top<T>::byte) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = capped<T>(v[i], byte[k]);
-    }
-    const uint32_t row = a.one_row ? 0u : id / per_row;
-    store16(y + (int64_t)row * p.stride + (int64_t)(id - row * per_row) * 16, v);
-  }
+  const uint32_t row = a.one_row ? 0u : id / per_row;
+  store16(y + (int64_t)row * p.stride + (int64_t)(id - row * per_row) * 16, v);
 }
 
 // Any width and alignment: one warp a group, one lane a value.
@@ -275,7 +251,7 @@ __global__ void __launch_bounds__(kCkptThreads) ckpt_unpack_any_kernel(const Ckp
 
 template <typename T, bool FP8>
 cudaError_t launch_ckpt_t(const CkptArgs& a, bool pack, cudaStream_t s) {
-  const uint64_t per_cta = a.wide ? (uint64_t)kCkptThreads * kCkptPieces : kCkptThreads / 32;
+  const uint64_t per_cta = a.wide ? (uint64_t)kCkptThreads : kCkptThreads / 32;
   const uint64_t units = (uint64_t)a.rows * (a.wide ? a.cols / 16 : (a.cols + 31) / 32);
   const dim3 grid((unsigned)((units + per_cta - 1) / per_cta), (unsigned)a.parts);
   if (pack && a.wide)
