@@ -10,20 +10,28 @@
 // score buffers of 64 keys, [128 m, +64) and [128 m + 64, +64).  A step is 64 keys:
 // P_m as bf16 takes the place of the step's scores, and the scores two steps on
 // follow P_m V in the issue order, so a map's softmax warps work on one buffer
-// while the tensor cores work on the other.  (Whole tiles of 128 keys in one
-// buffer each: 1,019 us against ... at 1.3B; products of 64 keys from shared memory
-// run at 48 cycles, not 32, but nobody waits for them.)
+// while the tensor cores work on the other.  (Score products of 64 keys run at 48
+// cycles, not 32: their operands come from shared memory at 128 bytes a cycle.)
 // Warp roles, 384 threads: warp 0 TMA producer (K and V rings of three tiles),
-// warp 1 tcgen05 issuer and owner of the tensor memory, warps 4-7 softmax of map
-// 1 and warps 8-11 of map 2, one thread a query row.  P enters its product as
-// bf16 (a choice: 2^-9 of each weight; the output's own rounding is as large); the
-// row sum and the log-sum-exp add the unrounded p.  At the end the two warp groups
-// exchange the row sums and each writes half of the features of its row.
+// warps 1 and 2 tcgen05 issuers of map 1 and 2 (warp 1 owns the tensor memory),
+// warps 4-7 softmax of map 1 and warps 8-11 of map 2, one thread a query row.  Two
+// issuers, because issuing slows the other warps of its scheduler.  At the end the
+// two warp groups exchange the row sums and each writes half of the features of its
+// row.
+// Roundings that are choices: P enters its product as bf16 (half a step, 2^-8 of
+// each weight at most, as much as the output's own rounding); the row sum and the
+// log-sum-exp add the unrounded p.
 //
-// Bound by the exponentials: 2 x 128 x 128 a tile pair, 16 a clock and SM on the
-// special-function unit, against 1,536 clocks of products at d = 128; one pair in
-// four therefore runs on the FMA pipe (exp2_fma_x2).  Every barrier wait is
-// bounded; on a time-out the kernel records it and drains.
+// Bound by the exponentials and their row work.  A step has 900 cycles of products
+// (384 scores, 512 P V, at d = 128) and 768 of the special-function unit, with one
+// pair of exponentials in four on the FMA pipe (exp2_fma_x2; 32,760 tokens x 12
+// heads of 128 at 90 % block sparsity, taken in turn: none 983 us, one in eight 932,
+// one in four and three in eight 914, one in two 924), and takes 1,500 (1.59 M active
+// cycles an SM over 1,068 steps, the ends of a CTA included).  The watch over
+// the cubic's range (softmax_pass) added 7 us to that, 927 -> 935 us taken in turn
+// on another box; 1,070 in a long run beside other work (0.99 TFLOP of products:
+// 1,060 and 930 TFLOP/s).  Every barrier wait is bounded; on a time-out the
+// kernel records it and drains.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -32,6 +40,7 @@ namespace {
 
 constexpr int kDiffThreads = 384;
 constexpr uint64_t kDiffDrainNs = 1000000000ull;
+constexpr float kDiffGrownLog2 = 60.f;
 constexpr float kDiffGrown = 1.152921504606847e18f;  // 2^60
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -107,10 +116,14 @@ __device__ __forceinline__ float row_max(uint32_t s_addr, int valid) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// p = 2^(s c + b) of 64 scores of the row as bf16 pairs; returns their sum.
-__device__ __forceinline__ float softmax_pass(uint32_t s_addr, int valid, uint64_t c2, float b, uint32_t (&pk)[32]) {
+// p = 2^(s c + b) of 64 scores of the row as bf16 pairs; returns their sum.  The cubic
+// wraps around for exponents from 128 on (to NaN, negative or small values, which no
+// sum shows), so `top` is the largest exponent that it was given.
+__device__ __forceinline__ float softmax_pass(uint32_t s_addr, int valid, uint64_t c2, float b, uint32_t (&pk)[32],
+                                              float& top) {
   const uint64_t b2 = f32x2_pack(b, b);
   uint64_t acc0 = 0, acc1 = 0;
+  top = -INFINITY;
   uint32_t sr[2][32];
   tmem_ld32(s_addr, sr[0]);
   tmem_ld32(s_addr + 32, sr[1]);
@@ -122,12 +135,12 @@ __device__ __forceinline__ float softmax_pass(uint32_t s_addr, int valid, uint64
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const uint64_t e = f32x2_fma(f32x2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, b2);
-      float p0, p1;
+      float p0, p1, x0, x1;
+      f32x2_unpack(e, x0, x1);
       if ((i & 3) == 3) {
         exp2_fma_x2(e, p0, p1);
+        top = fmax3(top, x0, x1);
       } else {
-        float x0, x1;
-        f32x2_unpack(e, x0, x1);
         p0 = ex2_approx(x0);
         p1 = ex2_approx(x1);
       }
@@ -306,13 +319,14 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       // The reference is the first step's maximum, and later steps' exponentials
       // are taken against it without looking for their own: fp32 and bf16 hold p
       // and its sums up to far above 2^60, and a row's precision does not depend
-      // on their common factor.  Only when a step's sum passes 2^60 does the row
+      // on their common factor.  Only when a step's sum or one weight passes 2^60 does the row
       // take the step's maximum as its new reference, with O and l scaled down and
       // the exponentials taken again (the scores are still there).
       if (u == 0) m_ref = row_max(buf, valid);
       uint32_t pk[32];
-      float rs = softmax_pass(buf, valid, c2, -m_ref * scale_log2, pk);
-      const bool grown = rs > kDiffGrown;
+      float top;
+      float rs = softmax_pass(buf, valid, c2, -m_ref * scale_log2, pk, top);
+      const bool grown = rs > kDiffGrown || top > kDiffGrownLog2;
       if (__any_sync(0xffffffffu, grown)) {
         const float mt = row_max(buf, valid);
         float alpha = 1.f;
@@ -333,7 +347,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
             tmem_st32(o_addr + 32 * c, pk);
           }
         }
-        rs = softmax_pass(buf, valid, c2, -m_ref * scale_log2, pk);
+        rs = softmax_pass(buf, valid, c2, -m_ref * scale_log2, pk, top);
       }
       l += rs;
       tmem_st32(buf, pk);  // over scores that have been read

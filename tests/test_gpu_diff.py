@@ -219,6 +219,52 @@ def test_gradients_against_differences():
         assert abs(slope - float((mine * step).sum())) <= lim, name
 
 
+# Per head and map: step of 64 keys -> (level, which of its keys carry it); a level is 2 units of score (nats) in a row
+# of amplitude 16.  One pair of keys in four has its exponential from the cubic: keys 6 and 7 of every 8.
+LEAPS = [
+    ({1: (31, "all")}, {}),
+    ({}, {1: (30, "all"), 3: (70, "one"), 5: (178, "all"), 10: (200, "all")}),
+    ({2: (45, "cubic")}, {4: (178, "cubic"), 6: (190, "cubic")}),
+    ({10: (100, "cubic")}, {10: (250, "one")}),
+]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_far_above_the_first_keys(d):
+    """Later keys whose scores pass the first keys' by up to 500 (2^721): in all keys of a step, in one, or only where the
+    cubic forms the exponential; several times, in one map or both, in the short last tile.
+
+    Scores of size S come from up to four matrix products, each off by 2^-23 of the largest term at most, and are stored
+    in fp32: off by 8 2^-23 S, a weight by twice that of itself (its own score and the sum's)."""
+    N, Hh = 680, len(LEAPS)
+    nb, c, S = -(-N // 128), d // 2, 500.0
+    keep = np.ones((Hh, nb, nb), bool)
+    q, k, v, dout, lam, rp, ci, trp, tci = make(1, N, Hh, d, keep, 31, lam_type=torch.float32)
+    scale = 0.125  # amplitude 16: a level is 2
+    amp = torch.tensor([16.0, 8.0, 0.0, -16.0, 16.0], device="cuda")[torch.arange(N, device="cuda") % 5]
+    for h, both in enumerate(LEAPS):
+        for m, steps in enumerate(both):
+            q[0, :, h, m * c] = amp.bfloat16()
+            k[0, :, h, m * c] = 0
+            for u, (level, which) in steps.items():
+                j = torch.arange(64 * u, min(64 * u + 64, N), device="cuda")
+                j = {"all": j, "one": j[5:6], "cubic": j[(j % 8) >= 6]}[which]
+                k[0, j, h, m * c] = level
+    kw = dict(softmax_scale=scale)
+    out, out2, lse = sl.diff_attn_forward_lse(q, k, v, rp, ci, lam, **kw)
+    more = 2 * 8 * 2.0 ** -23 * S
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    for h in range(Hh):
+        (p1, s1), (p2, s2) = maps(q, k, keep, scale, 0, h, False, Hh)
+        x, lh = v[0, :, h].double(), float(lam[h])
+        for got, ref, size in ((out, (p1 - lh * p2) @ x, (p1 + abs(lh) * p2) @ x.abs()), (out2, p2 @ x, p2 @ x.abs())):
+            lim = 2.0 ** -8 * ref.abs() + (2 * 2.0 ** -8 + 2e-4 + more) * size
+            assert bool(((got[0, :, h].double() - ref).abs() <= lim).all()), h
+        for m, s in enumerate((s1, s2)):
+            assert bool(((lse[m, 0, h].double() - s).abs() <= 2e-4 + 2.0 ** -18 * s.abs()).all()), (h, m)
+    assert torch.equal(out, sl.diff_attn_forward(q, k, v, rp, ci, lam, **kw))
+
+
 def test_what_is_not_kept_is_not_read():
     """Infinities and NaN in blocks that no row keeps do not reach the output or the gradients."""
     N, d = 512, 128
