@@ -118,7 +118,8 @@ __device__ __forceinline__ float row_max(uint32_t s_addr, int valid) {
 
 // p = 2^(s c + b) of 64 scores of the row as bf16 pairs; returns their sum.  The cubic
 // wraps around for exponents from 128 on (to NaN, negative or small values, which no
-// sum shows), so `top` is the largest exponent that it was given.
+// sum shows) and takes NaN for a large negative one, so `top` is the largest
+// exponent that it was given, NaN when one of them is.
 __device__ __forceinline__ float softmax_pass(uint32_t s_addr, int valid, uint64_t c2, float b, uint32_t (&pk)[32],
                                               float& top) {
   const uint64_t b2 = f32x2_pack(b, b);
@@ -139,7 +140,7 @@ __device__ __forceinline__ float softmax_pass(uint32_t s_addr, int valid, uint64
       f32x2_unpack(e, x0, x1);
       if ((i & 3) == 3) {
         exp2_fma_x2(e, p0, p1);
-        top = fmax3(top, x0, x1);
+        top = fmax3_nan(top, x0, x1);
       } else {
         p0 = ex2_approx(x0);
         p1 = ex2_approx(x1);
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       uint32_t pk[32];
       float top;
       float rs = softmax_pass(buf, valid, c2, -m_ref * scale_log2, pk, top);
-      const bool grown = rs > kDiffGrown || top > kDiffGrownLog2;
+      const bool grown = !(rs <= kDiffGrown && top <= kDiffGrownLog2);
       if (__any_sync(0xffffffffu, grown)) {
         const float mt = row_max(buf, valid);
         float alpha = 1.f;
@@ -348,6 +349,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
           }
         }
         rs = softmax_pass(buf, valid, c2, -m_ref * scale_log2, pk, top);
+        if (top != top) rs = top;  // a NaN among the scores is one of the row
       }
       l += rs;
       tmem_st32(buf, pk);  // over scores that have been read

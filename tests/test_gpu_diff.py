@@ -265,6 +265,24 @@ def test_scores_far_above_the_first_keys(d):
     assert torch.equal(out, sl.diff_attn_forward(q, k, v, rp, ci, lam, **kw))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at", [0, 6, 71, 130, 199])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_a_kept_key_without_a_value_shows(d, at, bad):
+    """NaN or infinity in one kept key (where the cubic forms its exponential and where not, in the first step, a later
+    one, the short last one) makes every row of that map NaN, as by the formula; the other head stays."""
+    keep = np.ones((2, 2, 2), bool)
+    q, k, v, _, lam, rp, ci, *_ = make(1, 200, 2, d, keep, 19)
+    clean = sl.diff_attn_forward(q, k, v, rp, ci, lam)
+    q[0, :, 0, 3] = 1.0  # (an infinite score is positive: its weight is inf / inf)
+    k[0, at, 0, 3] = bad
+    out, out2, lse = sl.diff_attn_forward_lse(q, k, v, rp, ci, lam)
+    assert bool(torch.isnan(out[0, :, 0]).all())
+    assert torch.equal(out[0, :, 1], clean[0, :, 1]) and bool(torch.isfinite(out2).all())
+    if math.isnan(bad):
+        assert bool(torch.isnan(lse[0, 0, 0]).all()) and bool(torch.isfinite(lse[1]).all())
+
+
 def test_what_is_not_kept_is_not_read():
     """Infinities and NaN in blocks that no row keeps do not reach the output or the gradients."""
     N, d = 512, 128
