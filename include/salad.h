@@ -511,7 +511,7 @@ typedef struct {
  *              apart (0: the same for all), or NULL: token n lies at
  *              origin + (n / (W H), n / W mod H, n mod W) with grid_h = H, grid_w
  *              = W (1, 1: one axis counting tokens); any int32 value.
- *   origin     HOST int32 [3], used when positions is NULL; NULL is (0, 0, 0).
+ *   origin     HOST int32 [3], used when positions is NULL, each at most 2^31 - N; NULL is (0, 0, 0).
  *   scale      finite factor of the turned pairs (1, or a long-context factor).
  * Angles are formed in fp64 and reduced before the fp32 sine and cosine; the
  * products are fp32 with one rounding to y's type.  Never synchronises, no

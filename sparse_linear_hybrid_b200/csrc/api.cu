@@ -833,6 +833,7 @@ int salad_rope(const salad_rope_tensor* tensors, int count, int x_type, int y_ty
     pairs += i < axes ? axis_pairs[i] : 0;
     a.axis_end[i] = (int)pairs;
     a.origin[i] = origin ? origin[i] : 0;
+    if (!positions && (long long)a.origin[i] + N > (1ll << 31)) return SALAD_ERR_INVALID_ARG;  // (positions are int32)
   }
   if (pairs != rot / 2) return SALAD_ERR_INVALID_ARG;
   const size_t xs = type_bytes(x_type), ys = type_bytes(y_type);

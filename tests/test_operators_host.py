@@ -24,7 +24,7 @@ def L():
 
 def rope(L, tensors=None, count=None, **kw):
     a = dict(x_type=1, y_type=1, B=1, N=8, d=64, rot=64, inter=0, freq=FAKE, pairs=(32,), axes=None, pos=None, pos_b=0,
-             gh=1, gw=1, scale=1.0, inverse=0)
+             gh=1, gw=1, origin=None, scale=1.0, inverse=0)
     a.update(kw)
     row = a["d"] * 2
     if tensors is None:
@@ -33,7 +33,7 @@ def rope(L, tensors=None, count=None, **kw):
     pairs = struct.pack("%di" % len(a["pairs"]), *a["pairs"])
     return L.salad_rope(packed, len(tensors) if count is None else count, a["x_type"], a["y_type"], a["B"], a["N"], a["d"],
                         a["rot"], a["inter"], a["freq"], pairs, len(a["pairs"]) if a["axes"] is None else a["axes"], a["pos"],
-                        a["pos_b"], a["gh"], a["gw"], None, a["scale"], a["inverse"], None)
+                        a["pos_b"], a["gh"], a["gw"], a["origin"], a["scale"], a["inverse"], None)
 
 
 def view(x, y, heads=2, n=8, d=64, sn=None, sb=None):
@@ -64,6 +64,11 @@ def test_rope_refusals(L):
     # side by side in one tensor, but reaching into each other
     assert rope(L, [view(0x10000000, 0x10000000, sn=384), view(0x10000000 + 128, 0x10000000 + 128, sn=384)]) == bad
     assert rope(L, [view(0x10000000, 0x20000000, sn=384), view(0x10000000 + 256, 0x20000000 + 640, sn=384)]) == bad
+
+
+def test_rope_positions_stay_within_int32(L):
+    for origin in ((2 ** 31 - 7, 0, 0), (0, 2 ** 31 - 1, 0), (0, 0, 2 ** 31 - 1)):
+        assert rope(L, origin=struct.pack("3i", *origin)) == sl.SALAD_ERR_INVALID_ARG
 
 
 def ckpt(L, fn="salad_ckpt_pack", tensors=None, rows=4, cols=64, type_=1, fmt=0, count=None):
