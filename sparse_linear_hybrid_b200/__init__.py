@@ -556,6 +556,17 @@ def _on(*tensors):
     return (_NULL if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)), tensors[0].device
 
 
+def _at(ctx, dev, stream):
+    """_on's context, or with a stream of the caller's the one that makes it
+    current: outputs and workspaces that the call allocates are then of that
+    stream, and are not given out again while its kernels use them."""
+    if stream is None:
+        return ctx
+    if stream.device != dev:
+        raise ValueError(f"the stream is of {stream.device}, the tensors of {dev}")
+    return torch.cuda.stream(stream)
+
+
 def _ptr(t, dtype, name) -> int:
     """_dev_ptr's checks for a tensor that _on has seen; the bare address."""
     if t.dtype != dtype:
@@ -610,7 +621,7 @@ def _rope(q, k, inv_freq, sections, interleaved, scale, positions, grid, origin,
     xs = (q,) if k is None else (q, k)
     if k is None and k_out is not None:
         raise ValueError("k_out without k")
-    ctx, _ = _on(*xs, inv_freq) if positions is None else _on(*xs, inv_freq, positions)
+    ctx, dev = _on(*xs, inv_freq) if positions is None else _on(*xs, inv_freq, positions)
     if q.dim() != 4:
         raise ValueError("q and k must be [B, N, heads, d] with the same B, N and d")
     B, N, _, d = q.shape
@@ -642,7 +653,7 @@ def _rope(q, k, inv_freq, sections, interleaved, scale, positions, grid, origin,
     elif axes != 1:
         raise ValueError("several sections need positions or a grid")
     ys, packed = [], b""
-    with ctx:
+    with _at(ctx, dev, stream):
         for x, y in zip(xs, (q_out, k_out)):
             if x.dim() != 4 or x.shape[0] != B or x.shape[1] != N or x.shape[3] != d:
                 raise ValueError("q and k must be [B, N, heads, d] with the same B, N and d")
@@ -761,9 +772,9 @@ def ckpt_pack(x, fmt: str = "int8", out=None, stream=None):
     outs = (None,) * len(xs) if out is None else out if many else (out,)
     if not xs or len(outs) != len(xs):
         raise ValueError("one output for each tensor")
-    ctx, _ = _on(*xs)
+    ctx, dev = _on(*xs)
     res = []
-    with ctx:
+    with _at(ctx, dev, stream):
         for t, c in zip(xs, outs):
             if t.dtype not in _TYPES or t.dim() < 1:
                 raise TypeError("tensors of fp32, bf16 or fp16 with one dimension at least")
@@ -793,9 +804,9 @@ def ckpt_unpack(ckpt, dtype=None, out=None, stream=None):
     fmt = cks[0].fmt
     if fmt not in _FORMATS or any(c.fmt != fmt for c in cks):
         raise ValueError("the checkpoints have several formats")
-    ctx, _ = _on(*(t for c in cks for t in (c.codes, c.scales)))
+    ctx, dev = _on(*(t for c in cks for t in (c.codes, c.scales)))
     res = []
-    with ctx:
+    with _at(ctx, dev, stream):
         for c, y in zip(cks, outs):
             _ptr(c.codes, torch.uint8, "codes"), _ptr(c.scales, torch.uint8, "scales")
             if c.scales.shape != _ckpt_scales_shape(c.codes.shape):
@@ -836,8 +847,9 @@ def attn_backward_ckpt(q, k, v, dout, row_ptr, col_idx, w_proj, gate, block: int
             raise ValueError("scales and codes have shapes that do not agree")
     if dout.shape != q.codes.shape or w_proj.shape != (d, d) or gate.shape != (B, Hh):
         raise ValueError("dout, w_proj or gate has another shape than the checkpoints ask for")
-    ctx, dev = _on(q.codes, q.scales, k.codes, k.scales, v.codes, v.scales, dout, row_ptr, col_idx, w_proj, gate)
-    with ctx:
+    ctx, dev = _on(q.codes, q.scales, k.codes, k.scales, v.codes, v.scales, dout, row_ptr, col_idx, w_proj, gate,
+                   *(t for t in (t_row_ptr, t_col_idx, workspace) if t is not None))
+    with _at(ctx, dev, stream):
         nb = (N + block - 1) // block
         if row_ptr.numel() != (B * Hh if mask_per_bh else Hh) * nb + 1:
             raise ValueError(f"row_ptr has {row_ptr.numel()} entries, not {(B * Hh if mask_per_bh else Hh) * nb + 1}")
@@ -901,7 +913,7 @@ def _mask_rows(row_ptr, B, N, heads, mask_per_bh):
 
 def _diff_forward(q, k, v, row_ptr, col_idx, lam, softmax_scale, mask_per_bh, out, out2, lse, train, workspace, stream):
     ctx, dev = _on(q, k, v, row_ptr, col_idx, lam, *(t for t in (out, out2, lse, workspace) if t is not None))
-    with ctx:
+    with _at(ctx, dev, stream):
         B, N, Hh, d = q.shape
         _mask_rows(row_ptr, B, N, Hh, mask_per_bh)
         if out is None:
@@ -915,7 +927,8 @@ def _diff_forward(q, k, v, row_ptr, col_idx, lam, softmax_scale, mask_per_bh, ou
             workspace = new_diff_workspace(B, N, Hh, d, dev)
         ptrs = _bf16_like(q, (q, "q"), (k, "k"), (v, "v"), (out, "out"), *([(out2, "out2")] if train else []))
         _check(lib().salad_diff_forward(
-            *ptrs[:3], B, N, Hh, d, 128, _ptr(row_ptr, torch.int32, "row_ptr"), _cols(col_idx, row_ptr), int(bool(mask_per_bh)), *_lam(lam, Hh), float(softmax_scale),
+            *ptrs[:3], B, N, Hh, d, 128, _ptr(row_ptr, torch.int32, "row_ptr"), _cols(col_idx, row_ptr),
+            int(bool(mask_per_bh)), *_lam(lam, Hh), float(softmax_scale),
             ptrs[3], ptrs[4] if train else None, _ptr(lse, torch.float32, "lse") if train else None,
             _ptr(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)), "salad_diff_forward")
     return out, out2, lse
@@ -948,7 +961,7 @@ def diff_attn_backward(q, k, v, out, out2, dout, lse, row_ptr, col_idx, lam, t_r
     diff_attn_forward_lse on the same inputs; the transposed mask as in attn_backward_sparse."""
     ctx, dev = _on(q, k, v, out, out2, dout, lse, row_ptr, col_idx, lam,
                    *(t for t in (t_row_ptr, t_col_idx, workspace) if t is not None))
-    with ctx:
+    with _at(ctx, dev, stream):
         B, N, Hh, d = q.shape
         _mask_rows(row_ptr, B, N, Hh, mask_per_bh)
         t_row_ptr, t_col_idx = _transposed_mask(row_ptr, col_idx, t_row_ptr, t_col_idx,
@@ -975,8 +988,8 @@ def diff_attn_decode(q, k_cache, v_cache, lens, lam, softmax_scale: float = 0.0,
     """Differential attention of a few queries against a cache (see salad_diff_decode):
     q bf16 [B, Nq, Hh, d], k_cache and v_cache bf16 [B, capacity, Hh, d], lens int32
     CUDA [B]; every query of sequence b sees keys [0, lens[b])."""
-    ctx, _ = _on(q, k_cache, v_cache, lens, lam, *(() if out is None else (out,)))
-    with ctx:
+    ctx, dev = _on(q, k_cache, v_cache, lens, lam, *(() if out is None else (out,)))
+    with _at(ctx, dev, stream):
         B, Nq, Hh, d = q.shape
         cap = k_cache.shape[1]
         if k_cache.shape != (B, cap, Hh, d) or v_cache.shape != k_cache.shape or lens.shape != (B,):

@@ -397,6 +397,31 @@ def test_training_step_in_a_graph():
     assert sl.check_status(ws) == sl.SALAD_OK and sl.check_status(other) == sl.SALAD_OK
 
 
+def test_what_a_call_allocates_is_of_its_stream():
+    """A call on a stream that is still busy: its workspace, dropped when the call returns, may not be given to a tensor
+    of the current stream, and its results are those of the current stream's call."""
+    B, N, Hh, d = 1, 700, 2, 64
+    nb = -(-N // 128)
+    q, k, v, dout, lam, rp, ci, trp, tci = make(B, N, Hh, d, np.ones((Hh, nb, nb), bool), 6)
+    w, gate = torch.zeros(d, d, device="cuda").bfloat16(), torch.ones(B, Hh, device="cuda")
+    kept = sl.ckpt_pack([q, k, v])
+    out, out2, lse = sl.diff_attn_forward_lse(q, k, v, rp, ci, lam)
+    calls = (
+        (sl.new_diff_workspace(B, N, Hh, d).numel(), lambda **kw: sl.diff_attn_backward(q, k, v, out, out2, dout, lse, rp, ci, lam, **kw)),
+        (sl.new_ckpt_backward_workspace(B, N, Hh, d).numel(), lambda **kw: sl.attn_backward_ckpt(*kept, dout, rp, ci, w, gate, **kw)))
+    side = torch.cuda.Stream()
+    for size, call in calls:
+        want = call()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)  # a tenth of a second or so
+        got = call(stream=side)
+        mine = torch.full((size,), 7, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        assert bool((mine == 7).all())
+        assert all(torch.equal(want[n], got[n]) for n in want)
+
+
 def test_a_wait_that_runs_out_is_reported():
     """With a limit of 0 every wait that is not already satisfied fails at once: an error status, no hang."""
     keep = np.ones((2, 3, 3), bool)
