@@ -599,7 +599,7 @@ int salad_attn_backward_ckpt(const uint8_t* q_codes, const uint8_t* q_scales, co
  * Outputs may not overlap inputs or each other.  Arithmetic: bf16 tensor-core
  * products with fp32 accumulation, p rounded to bf16 for its product, fp32
  * softmax, one rounding of each output.  Never synchronises.  Errors:
- * INVALID_ARG, UNSUPPORTED (d, block, 2^31 query tiles), WORKSPACE, CUDA.
+ * INVALID_ARG, UNSUPPORTED (d, block, B*Hh*ceil(N/128) >= 2^24), WORKSPACE, CUDA.
  */
 size_t salad_diff_workspace_bytes(int B, int N, int num_heads, int d);
 int salad_diff_forward(const void* q, const void* k, const void* v, int B, int N, int num_heads, int d, int block,
