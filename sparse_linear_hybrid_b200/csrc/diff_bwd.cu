@@ -23,13 +23,12 @@
 //   diff_dlam_kernel  sums the shares of every head in a fixed order
 // Gradients are rounded once, to bf16 (dlam to lam's type).  P and dS enter their
 // products as bf16, a choice: half a step of each weight, averaged over the sum.
-// Of one 9,450-token step of 12 heads of 128 (forward and backward 949 us a call)
-// the prep takes 21 us, dQ 326, dK/dV 399, by themselves; the tensor cores are
+// Of one 9,360-token step of 12 heads of 128 (forward and backward 949 to 1,025 us
+// a call by box) the prep takes 21 us, dQ 326, dK/dV 399, by themselves; the tensor cores are
 // busy 45 and 49 % of that.  dK/dV is bound by shared memory (its products read
 // both operands from there, dS_2^T passes through it), dQ by the row warps.  One
 // pair of exponentials in four on the FMA pipe (949 us; none 955, one in two 986).
-// Warp roles, 384
-// threads: warp 0 TMA producer, warps 1-3 tcgen05 issuers (warp 1 owns the tensor
+// Warp roles, 384 threads: warp 0 TMA producer, warps 1-3 tcgen05 issuers (warp 1 owns the tensor
 // memory), warps 4-11 the rows (TMEM lane quarter = warp % 4).  There are several
 // issuers because a warp that pushes products into a full tensor-core queue holds
 // up the shared-memory instructions of its scheduler's other warps: with one
