@@ -19,8 +19,9 @@
 // two warp groups exchange the row sums and each writes half of the features of its
 // row.
 // Roundings that are choices: P enters its product as bf16 (half a step, 2^-8 of
-// each weight at most, as much as the output's own rounding); the row sum and the
-// log-sum-exp add the unrounded p.
+// each weight at most, as much as the output's own rounding), and the sum that O is
+// divided by adds the same rounded p: a weight that holds its row is exact.  The
+// log-sum-exp adds the unrounded p.
 //
 // Bound by the exponentials and their row work.  A step has 900 cycles of products
 // (384 scores, 512 P V, at d = 128) and 768 of the special-function unit, with one
@@ -116,14 +117,16 @@ __device__ __forceinline__ float row_max(uint32_t s_addr, int valid) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// p = 2^(s c + b) of 64 scores of the row as bf16 pairs; returns their sum.  The cubic
-// wraps around for exponents from 128 on (to NaN, negative or small values, which no
-// sum shows) and takes NaN for a large negative one, so `top` is the largest
-// exponent that it was given, NaN when one of them is.
+// p = 2^(s c + b) of 64 scores of the row as bf16 pairs; returns the sum of those, and
+// with TRAIN in `exact` the sum before the rounding.  The cubic wraps around for
+// exponents from 128 on (to NaN, negative or small values, which no sum shows) and
+// takes NaN for a large negative one, so `top` is the largest exponent that it was
+// given, NaN when one of them is.
+template <bool TRAIN>
 __device__ __forceinline__ float softmax_pass(uint32_t s_addr, int valid, uint64_t c2, float b, uint32_t (&pk)[32],
-                                              float& top) {
+                                              float& top, float& exact) {
   const uint64_t b2 = f32x2_pack(b, b);
-  uint64_t acc0 = 0, acc1 = 0;
+  uint64_t acc0 = 0, acc1 = 0, full = 0;
   top = -INFINITY;
   uint32_t sr[2][32];
   tmem_ld32(s_addr, sr[0]);
@@ -145,14 +148,18 @@ __device__ __forceinline__ float softmax_pass(uint32_t s_addr, int valid, uint64
         p0 = ex2_approx(x0);
         p1 = ex2_approx(x1);
       }
-      pk[16 * c + i] = pack_bf16x2(p0, p1);
+      const uint32_t w = pack_bf16x2(p0, p1);
+      pk[16 * c + i] = w;
       if (i & 1)
-        acc1 = f32x2_add(acc1, f32x2_pack(p0, p1));
+        acc1 = f32x2_add(acc1, f32x2_pack(bf16_lo_to_f32(w), bf16_hi_to_f32(w)));
       else
-        acc0 = f32x2_add(acc0, f32x2_pack(p0, p1));
+        acc0 = f32x2_add(acc0, f32x2_pack(bf16_lo_to_f32(w), bf16_hi_to_f32(w)));
+      if (TRAIN) full = f32x2_add(full, f32x2_pack(p0, p1));
     }
   }
   float a0, a1;
+  f32x2_unpack(full, a0, a1);
+  exact = a0 + a1;
   f32x2_unpack(f32x2_add(acc0, acc1), a0, a1);
   return a0 + a1;
 }
@@ -310,7 +317,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t s_addr = lane_addr + C::TM_S + 128 * m, o_addr = lane_addr + C::TM_O + 128 * m;
     const uint64_t c2 = f32x2_pack(scale_log2, scale_log2);
-    float m_ref = -INFINITY, l = 0.f;
+    float m_ref = -INFINITY, l = 0.f, lx = 0.f;  // (lx: for the log-sum-exp)
     bool ok = limit_ns != 0;
     for (int u = 0; u < steps; ++u) {
       const uint32_t buf = s_addr + 64 * (u & 1);
@@ -325,8 +332,8 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       // the exponentials taken again (the scores are still there).
       if (u == 0) m_ref = row_max(buf, valid);
       uint32_t pk[32];
-      float top;
-      float rs = softmax_pass(buf, valid, c2, -m_ref * scale_log2, pk, top);
+      float top, rx;
+      float rs = softmax_pass<TRAIN>(buf, valid, c2, -m_ref * scale_log2, pk, top, rx);
       const bool grown = !(rs <= kDiffGrown && top <= kDiffGrownLog2);
       if (__any_sync(0xffffffffu, grown)) {
         const float mt = row_max(buf, valid);
@@ -336,6 +343,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
           m_ref = mt;
         }
         l *= alpha;
+        lx *= alpha;
         if (u > 0) {
           mbar_await(&sh->pv_done[m], (uint32_t)((u - 1) & 1), polls, ok);
           tc_fence_after();
@@ -348,10 +356,11 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
             tmem_st32(o_addr + 32 * c, pk);
           }
         }
-        rs = softmax_pass(buf, valid, c2, -m_ref * scale_log2, pk, top);
-        if (top != top) rs = top;  // a NaN among the scores is one of the row
+        rs = softmax_pass<TRAIN>(buf, valid, c2, -m_ref * scale_log2, pk, top, rx);
+        if (top != top) rs = rx = top;  // a NaN among the scores is one of the row
       }
       l += rs;
+      lx += rx;
       tmem_st32(buf, pk);  // over scores that have been read
       tmem_st_wait();
       tc_fence_before();
@@ -364,7 +373,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
     const int row = qt * 128 + r;
     if (TRAIN && ok && row < N) {
       const size_t BH = gridDim.x / nb;
-      lse[((size_t)m * BH + bh) * N + row] = n > 0 ? (m_ref * scale_log2 + log2f(l)) * kLn2 : -INFINITY;
+      lse[((size_t)m * BH + bh) * N + row] = n > 0 ? (m_ref * scale_log2 + log2f(lx)) * kLn2 : -INFINITY;
     }
     sh->sum[m][r] = l;
     named_bar_sync(1, 256);  // (reached by every softmax thread, after a time-out too)
