@@ -41,3 +41,25 @@ def test_one_weight_that_holds_a_row_is_exact(late, d):
     out, out2, lse = sl.diff_attn_forward_lse(q, k, v, rp, ci, torch.zeros(1, device="cuda"), softmax_scale=1.0)
     assert torch.equal(out, want) and torch.equal(out2, want)
     assert torch.equal(out, sl.diff_attn_forward(q, k, v, rp, ci, torch.zeros(1, device="cuda"), softmax_scale=1.0))
+
+
+# keys of score -inf in map 1 (in map 2 for the second head)
+DECODE = {"one key": ([0], 1), "alone in its slot": ([4], 5), "the first ones": (list(range(40)), 300),
+          "all but one": ([j for j in range(517) if j != 300], 517), "every other": (list(range(0, 2000, 2)), 2000),
+          "the last run": (list(range(1990, 2000)), 2000)}
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq", [1, 2, 3])
+@pytest.mark.parametrize("name", DECODE)
+def test_decode_weighs_a_score_of_minus_infinity_with_nothing(name, Nq, d):
+    at, n = DECODE[name]
+    g = torch.Generator(device="cuda").manual_seed(n + d)
+    q, k, v = (torch.randn(1, m, 2, d, generator=g, device="cuda").bfloat16() for m in (Nq, n + 3, n + 3))
+    q[0, :, 0, 3], q[0, :, 1, d // 2 + 3] = 1.0, 1.0
+    k[0, at, 0, 3], k[0, at, 1, d // 2 + 3] = -math.inf, -math.inf
+    lam = torch.tensor([0.5, 0.8], device="cuda")
+    out = sl.diff_attn_decode(q, k, v, torch.tensor([n], dtype=torch.int32, device="cuda"), lam)
+    ref, size = decode_reference(q, k, v, [n], lam)  # (a map whose keys all score -inf: 0 / 0, NaN, as by the formula)
+    assert torch.equal(torch.isnan(out), torch.isnan(ref)) and bool(torch.isnan(ref).any()) == (n == 1)
+    assert n == 1 or bool(((out.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 1e-5 * size).all())
