@@ -236,9 +236,9 @@ __global__ void __launch_bounds__(32 * kDecWarps, DecCfg<NQ>::CTAS)
         l += g * pl[c];
         acc += g * pa[c];
       }
-      o[x] = len > 0 ? acc / l : 0.f;
+      o[x] = acc / l;
     }
-    const uint32_t y = pack_bf16x2(fmaf(-lam, o[1], o[0]), 0.f);
+    const uint32_t y = len > 0 ? pack_bf16x2(fmaf(-lam, o[1], o[0]), 0.f) : 0u;
     a.out[(((int64_t)b * a.Nq + q0 + i) * a.heads + h) * D + f] = (uint16_t)(y & 0xFFFFu);
   }
   cluster.sync();  // a CTA's shared memory outlives its last reader

@@ -63,3 +63,10 @@ def test_decode_weighs_a_score_of_minus_infinity_with_nothing(name, Nq, d):
     ref, size = decode_reference(q, k, v, [n], lam)  # (a map whose keys all score -inf: 0 / 0, NaN, as by the formula)
     assert torch.equal(torch.isnan(out), torch.isnan(ref)) and bool(torch.isnan(ref).any()) == (n == 1)
     assert n == 1 or bool(((out.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 1e-5 * size).all())
+
+
+@pytest.mark.parametrize("lam", [math.inf, math.nan])
+def test_a_sequence_without_keys_is_zero_for_every_lambda(lam):
+    q, k, v = (torch.randn(2, n, 1, 64, device="cuda").bfloat16() for n in (1, 9, 9))
+    out = sl.diff_attn_decode(q, k, v, torch.tensor([0, 5], dtype=torch.int32, device="cuda"), torch.full((1,), lam, device="cuda"))
+    assert bool((out[0] == 0).all()) and not bool(torch.isfinite(out[1]).any())
