@@ -329,17 +329,19 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       // and its sums up to far above 2^60, and a row's precision does not depend
       // on their common factor.  Only when a step's sum or one weight passes 2^60 does the row
       // take the step's maximum as its new reference, with O and l scaled down and
-      // the exponentials taken again (the scores are still there).
+      // the exponentials taken again (the scores are still there).  So does a row
+      // whose scores were all -inf so far: it has no reference yet, and its weights of
+      // 0 are taken against 0.
       if (u == 0) m_ref = row_max(buf, valid);
       uint32_t pk[32];
       float top, rx;
-      float rs = softmax_pass<TRAIN>(buf, valid, c2, -m_ref * scale_log2, pk, top, rx);
-      const bool grown = !(rs <= kDiffGrown && top <= kDiffGrownLog2);
+      float rs = softmax_pass<TRAIN>(buf, valid, c2, m_ref == -INFINITY ? 0.f : -m_ref * scale_log2, pk, top, rx);
+      const bool grown = !(rs <= kDiffGrown && top <= kDiffGrownLog2 && m_ref > -INFINITY);
       if (__any_sync(0xffffffffu, grown)) {
         const float mt = row_max(buf, valid);
         float alpha = 1.f;
-        if (grown) {
-          alpha = ex2_approx((m_ref - mt) * scale_log2);
+        if (grown && mt > -INFINITY) {
+          alpha = ex2_approx((m_ref - mt) * scale_log2);  // (0 where there was none)
           m_ref = mt;
         }
         l *= alpha;
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
             tmem_st32(o_addr + 32 * c, pk);
           }
         }
-        rs = softmax_pass<TRAIN>(buf, valid, c2, -m_ref * scale_log2, pk, top, rx);
+        rs = softmax_pass<TRAIN>(buf, valid, c2, m_ref == -INFINITY ? 0.f : -m_ref * scale_log2, pk, top, rx);
         if (top != top) rs = rx = top;  // a NaN among the scores is one of the row
       }
       l += rs;
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       const size_t BH = gridDim.x / nb;
       lse[((size_t)m * BH + bh) * N + row] = n > 0 ? (m_ref * scale_log2 + log2f(lx)) * kLn2 : -INFINITY;
     }
-    sh->sum[m][r] = l;
+    sh->sum[m][r] = m_ref == -INFINITY ? NAN : l;  // (kept keys that all score -inf: 0 / 0)
     named_bar_sync(1, 256);  // (reached by every softmax thread, after a time-out too)
     tc_fence_after();
     // features [m D/2, m D/2 + D/2) of this row: out = O_1 / l_1 - lam O_2 / l_2

@@ -70,3 +70,37 @@ def test_a_sequence_without_keys_is_zero_for_every_lambda(lam):
     q, k, v = (torch.randn(2, n, 1, 64, device="cuda").bfloat16() for n in (1, 9, 9))
     out = sl.diff_attn_decode(q, k, v, torch.tensor([0, 5], dtype=torch.int32, device="cuda"), torch.full((1,), lam, device="cuda"))
     assert bool((out[0] == 0).all()) and not bool(torch.isfinite(out[1]).any())
+
+
+# keys of score -inf among 200: whole steps of 64, all but the cubic's positions, all but the last key
+FORWARD = {"first step": range(64), "two steps and more": range(131), "all but the last": range(199), "first key": [0],
+           "every other": range(0, 200, 2), "cubic": [j for j in range(200) if j % 8 >= 6],
+           "all but the cubic's": [j for j in range(200) if j % 8 < 6], "the short last step": range(192, 200)}
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("name", FORWARD)
+def test_forward_weighs_a_score_of_minus_infinity_with_nothing(name, d):
+    keep = np.ones((2, 2, 2), bool)
+    q, k, v, _, lam, rp, ci, *_ = make(1, 200, 2, d, keep, 23, lam_type=torch.float32)
+    q[0, :, 0, 3], q[0, :, 1, d // 2 + 3] = 1.0, 1.0
+    at = list(FORWARD[name])
+    k[0, at, 0, 3], k[0, at, 1, d // 2 + 3] = -math.inf, -math.inf
+    out, out2, lse = sl.diff_attn_forward_lse(q, k, v, rp, ci, lam)
+    assert bool(torch.isfinite(out).all())
+    check_forward(q, k, v, keep, lam, out, out2, lse, False)
+    assert torch.equal(out, sl.diff_attn_forward(q, k, v, rp, ci, lam))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 64, 200])
+def test_a_row_of_scores_of_minus_infinity_has_no_value(n, d):
+    """Kept keys that all score -inf: 0 / 0 by the formula, and a log-sum-exp of -inf.  (No kept key at all: 0.)"""
+    nb = -(-n // 128)
+    q, k, v, _, lam, rp, ci, *_ = make(1, n, 2, d, np.ones((2, nb, nb), bool), 24)
+    clean = sl.diff_attn_forward_lse(q, k, v, rp, ci, lam)
+    q[0, :, 0, 3] = 1.0
+    k[0, :, 0, 3] = -math.inf
+    out, out2, lse = sl.diff_attn_forward_lse(q, k, v, rp, ci, lam)
+    assert bool(torch.isnan(out[0, :, 0]).all()) and bool((lse[0, 0, 0] == -math.inf).all())
+    assert all(torch.equal(a, b) for a, b in ((out[:, :, 1], clean[0][:, :, 1]), (out2, clean[1]), (lse[1], clean[2][1])))
