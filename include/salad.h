@@ -598,7 +598,9 @@ int salad_attn_backward_ckpt(const uint8_t* q_codes, const uint8_t* q_scales, co
  *                 read it with salad_check_status).
  * Outputs may not overlap inputs or each other.  Arithmetic: bf16 tensor-core
  * products with fp32 accumulation, p rounded to bf16 for its product, fp32
- * softmax, one rounding of each output.  Never synchronises.  Errors:
+ * softmax, one rounding of each output.  The sums hold p v with p up to 2^24:
+ * |v| up to 2^88.  A row whose kept keys all score -inf is NaN, as by the
+ * formula.  Never synchronises.  Errors:
  * INVALID_ARG, UNSUPPORTED (d, block, B*Hh*ceil(N/128) >= 2^24), WORKSPACE, CUDA.
  */
 size_t salad_diff_workspace_bytes(int B, int N, int num_heads, int d);

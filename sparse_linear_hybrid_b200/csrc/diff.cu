@@ -41,8 +41,10 @@ namespace {
 
 constexpr int kDiffThreads = 384;
 constexpr uint64_t kDiffDrainNs = 1000000000ull;
-constexpr float kDiffGrownLog2 = 60.f;
-constexpr float kDiffGrown = 1.152921504606847e18f;  // 2^60
+// What a weight and a step's sum of weights may grow to.  O = sum p v has to stay in
+// fp32's range: with 2^15 steps (2 million keys) it does for values up to 2^88.
+constexpr float kDiffGrownLog2 = 24.f;
+constexpr float kDiffGrown = 16777216.f;  // 2^24
 constexpr float kLn2 = 0.69314718055994531f;
 
 struct DiffShared {
@@ -326,8 +328,8 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       tc_fence_after();
       // The reference is the first step's maximum, and later steps' exponentials
       // are taken against it without looking for their own: fp32 and bf16 hold p
-      // and its sums up to far above 2^60, and a row's precision does not depend
-      // on their common factor.  Only when a step's sum or one weight passes 2^60 does the row
+      // and its sums up to far above 2^24, and a row's precision does not depend
+      // on their common factor.  Only when a step's sum or one weight passes 2^24 does the row
       // take the step's maximum as its new reference, with O and l scaled down and
       // the exponentials taken again (the scores are still there).  So does a row
       // whose scores were all -inf so far: it has no reference yet, and its weights of

@@ -104,3 +104,31 @@ def test_a_row_of_scores_of_minus_infinity_has_no_value(n, d):
     out, out2, lse = sl.diff_attn_forward_lse(q, k, v, rp, ci, lam)
     assert bool(torch.isnan(out[0, :, 0]).all()) and bool((lse[0, 0, 0] == -math.inf).all())
     assert all(torch.equal(a, b) for a, b in ((out[:, :, 1], clean[0][:, :, 1]), (out2, clean[1]), (lse[1], clean[2][1])))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_values_beside_scores_far_above_the_first_keys(d):
+    """Values up to 2^88 in rows whose later scores pass the first keys' by 2^10 to 2^110: sums stay in fp32's range, as
+    the output does.  Scores of up to 90 are off by 8 2^-23 90 each, a weight by twice that."""
+    N, top = 680, 2.0 ** 88
+    keep = np.ones((2, 6, 6), bool)
+    q, k, v, _, _, rp, ci, *_ = make(1, N, 2, d, keep, 41)
+    lam = torch.tensor([0.5, -0.25], device="cuda")
+    v = (v.float().clamp(-1, 1) * top).bfloat16()
+    scale, amp = 0.125, torch.tensor([16.0, 8.0, 4.0, 2.0, 0.0], device="cuda")[torch.arange(N, device="cuda") % 5]
+    for h in range(2):
+        for m in range(2):
+            at = m * (d // 2)
+            q[0, :, h, at] = amp.bfloat16()
+            k[0, :, h, at] = 0
+            k[0, 64:, h, at] = 4 + 3.0 * (h + m)      # 2^11 to 2^29 above the first step at the amplitude 16
+            k[0, 400:, h, at] = 30                    # 2^87
+            k[0, 601 + h, h, at] = 38                 # 2^110, in one key
+    out, out2, lse = sl.diff_attn_forward_lse(q, k, v, rp, ci, lam, softmax_scale=scale)
+    more = 2 * 8 * 2.0 ** -23 * 90
+    for h in range(2):
+        (p1, _), (p2, _) = maps(q, k, keep, scale, 0, h, False, 2)
+        x, lh = v[0, :, h].double(), float(lam[h])
+        for got, ref, size in ((out, (p1 - lh * p2) @ x, (p1 + abs(lh) * p2) @ x.abs()), (out2, p2 @ x, p2 @ x.abs())):
+            lim = 2.0 ** -8 * ref.abs() + (2 * 2.0 ** -8 + 2e-4 + more) * size
+            assert bool(((got[0, :, h].double() - ref).abs() <= lim).all()), h
