@@ -8,7 +8,7 @@
 // The maps share dp and dv, so a pair of tiles costs the same products as one
 // plain attention head of width d; the exponentials are doubled.
 //   diff_prep_kernel  D_1, D_2 and the log-sum-exps in base 2, rows padded to
-//                     whole tiles (pad rows: p = 0)
+//                     whole tiles (pad rows: 1e30, finite, for p = 0)
 //   diff_dq_kernel    one CTA per (query tile, b, h), 64 keys a step in two buffers
 //                     of tensor memory: S_1, S_2 and dP, then dS_1 and dS_2 as bf16
 //                     over S_1; one thread a row and half of the step's keys; and
@@ -44,6 +44,7 @@ namespace {
 constexpr int kDiffBwdThreads = 384;
 constexpr uint64_t kDiffBwdDrainNs = 1000000000ull;
 constexpr float kDiffLog2e = 1.4426950408889634f;
+constexpr float kDiffPadLse = 1e30f;
 
 struct DiffBwdShared {
   uint64_t fixed_full;
@@ -101,7 +102,7 @@ __device__ __forceinline__ void mma_steps(uint32_t d_tmem, uint32_t x, uint32_t 
   }
 }
 
-// rows[B*Hh][npad/64][4][64]: lse_1 and lse_2 (base 2; +inf in pad rows), D_1, D_2
+// rows[B*Hh][npad/64][4][64]: lse_1 and lse_2 (base 2; kDiffPadLse in pad rows), D_1, D_2
 // of 64 queries, the piece that a step of the dK/dV kernel loads.
 // D/8 lanes a row, eight features a lane.
 template <int D>
@@ -138,8 +139,8 @@ __global__ void __launch_bounds__(256)
   if (part == 0) {
     const int64_t BH = (int64_t)B * heads;
     float* at = rows + bh * npad * 4 + n / 64 * 256 + n % 64;
-    at[0] = n < N ? lse[bh * N + n] * kDiffLog2e : INFINITY;
-    at[64] = n < N ? lse[(BH + bh) * N + n] * kDiffLog2e : INFINITY;
+    at[0] = n < N ? lse[bh * N + n] * kDiffLog2e : kDiffPadLse;
+    at[64] = n < N ? lse[(BH + bh) * N + n] * kDiffLog2e : kDiffPadLse;
     at[128] = fmaf(diff_lambda(lam, lam_bf16, h), d2, d0);
     at[192] = d2;
   }
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
     const float lh = diff_lambda(lam, lam_bf16, h);
     const uint64_t c2 = f32x2_pack(scale_log2, scale_log2), nlam = f32x2_pack(-lh, -lh);
-    const uint64_t minus = f32x2_pack(-1.f, -1.f);
+    const uint64_t minus = f32x2_pack(-1.f, -1.f), zero = f32x2_pack(0.f, 0.f);
     bool ok = limit_ns != 0;
     for (int i = 0; i < 2 * n; ++i) {
       const int s = i % C::STAGES;
@@ -580,7 +581,15 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
             q0 = ex2_approx(y0);
             q1 = ex2_approx(y1);
           }
-          const uint64_t p = f32x2_pack(p0, p1), q = f32x2_pack(q0, q1), gi = pair_of(g, k + u);
+          uint64_t p = f32x2_pack(p0, p1), q = f32x2_pack(q0, q1);
+          const uint64_t gi = pair_of(g, k + u);
+          if (((k + u) & 3) == 3) {
+            // The cubic takes a NaN for a large negative exponent.  A query with one has
+            // a log-sum-exp that is not finite, and 0 times that brings the NaN back
+            // (dq and dk have it through D, dv has it from here).
+            p = f32x2_fma(row(0), zero, p);
+            q = f32x2_fma(row(1), zero, q);
+          }
           a[k + u] = pack_pair(f32x2_fma(nlam, q, p));
           z1[k + u] = pack_pair(f32x2_mul(p, f32x2_fma(row(2), minus, gi)));
           z2[k + u] = pack_pair(f32x2_mul(q, f32x2_fma(row(3), minus, gi)));

@@ -132,3 +132,31 @@ def test_large_values_beside_scores_far_above_the_first_keys(d):
         for got, ref, size in ((out, (p1 - lh * p2) @ x, (p1 + abs(lh) * p2) @ x.abs()), (out2, p2 @ x, p2 @ x.abs())):
             lim = 2.0 ** -8 * ref.abs() + (2 * 2.0 ** -8 + 2e-4 + more) * size
             assert bool(((got[0, :, h].double() - ref).abs() <= lim).all()), h
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("at", [0, 5, 6, 7, 70, 150, 199])
+@pytest.mark.parametrize("bad,map_", [(math.nan, 0), (math.nan, 1), (math.inf, 0)])
+def test_a_query_without_a_value_shows_in_every_gradient(d, at, bad, map_):
+    """NaN or infinity in one query: its dq, and dk and dv of every key that it keeps, are NaN by the formula, wherever the
+    cubic forms its exponentials; keys that it does not keep, and the other head, stay."""
+    keep = np.ones((2, 2, 2), bool)
+    keep[0] = [[True, True], [False, True]]  # the second block of queries does not keep the first block of keys
+    q, k, v, dout, lam, rp, ci, trp, tci = make(1, 200, 2, d, keep, 29)
+    kw = dict(t_row_ptr=trp, t_col_idx=tci)
+
+    def gradients():
+        out, out2, lse = sl.diff_attn_forward_lse(q, k, v, rp, ci, lam)
+        return sl.diff_attn_backward(q, k, v, out, out2, dout, lse, rp, ci, lam, **kw)
+    clean = gradients()
+    q[0, at, 0, map_ * (d // 2) + 3] = bad
+    got = gradients()
+    kept = slice(0, 200) if at < 128 else slice(128, 200)
+    half = slice(map_ * (d // 2), (map_ + 1) * (d // 2))
+    assert bool(torch.isnan(got["dq"][0, at, 0, half]).all())
+    assert bool(torch.isnan(got["dv"][0, kept, 0]).all()) and bool(torch.isnan(got["dk"][0, kept, 0, half]).all())
+    assert bool(torch.isnan(got["dlam"][0])) == (map_ == 1)
+    if at >= 128:
+        assert all(torch.equal(got[n][0, :128, 0], clean[n][0, :128, 0]) for n in ("dq", "dk", "dv"))
+    assert all(torch.equal(got[n][0, :, 1], clean[n][0, :, 1]) for n in ("dq", "dk", "dv"))
+    assert torch.equal(got["dlam"][1], clean["dlam"][1])
