@@ -617,8 +617,10 @@ int salad_diff_forward(const void* q, const void* k, const void* v, int B, int N
  *   out, out2, lse  from salad_diff_forward with the same inputs; dout DEVICE bf16.
  *   t_row_ptr, t_col_idx  the transposed mask (as salad_attn_backward_sparse).
  *   dq, dk, dv  DEVICE bf16 [B][N][Hh][d], 16-byte aligned;  dlam DEVICE [Hh] of lam_type.
- * Sums are fp32 in a fixed order (deterministic), rounded once.  Other
- * arguments, workspace and errors as salad_diff_forward.
+ * Sums are fp32 in a fixed order (deterministic), rounded once.  An infinite key
+ * makes dq NaN by the formula (0 times it), and may make its own dk and dv NaN; the
+ * other keys' and dlam are the formula's.  Other arguments, workspace and errors as
+ * salad_diff_forward.
  */
 int salad_diff_backward(const void* q, const void* k, const void* v, const void* out, const void* out2,
                         const void* dout, const float* lse, int B, int N, int num_heads, int d, int block,

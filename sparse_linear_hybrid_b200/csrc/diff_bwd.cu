@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     }
     float dl, dl_odd;
     f32x2_unpack(dl2, dl, dl_odd);
-    dl += dl_odd;
+    dl = qt * 128 + r < N ? dl + dl_odd : 0.f;  // (a row behind the last: 0 times an infinite key is NaN)
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) dl += __shfl_xor_sync(0xffffffffu, dl, o);
     if (lane == 0) sh->part[warp - 4] = dl;

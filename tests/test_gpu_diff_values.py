@@ -160,3 +160,23 @@ def test_a_query_without_a_value_shows_in_every_gradient(d, at, bad, map_):
         assert all(torch.equal(got[n][0, :128, 0], clean[n][0, :128, 0]) for n in ("dq", "dk", "dv"))
     assert all(torch.equal(got[n][0, :, 1], clean[n][0, :, 1]) for n in ("dq", "dk", "dv"))
     assert torch.equal(got["dlam"][1], clean["dlam"][1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N", [200, 330])
+def test_gradients_beside_a_score_of_minus_infinity(N, d):
+    """A key that scores -inf for every query weighs nothing: dlam and the other keys' dk and dv are those of the formula,
+    also where the last tile of queries is short (dq is 0 times the infinite key, NaN)."""
+    nb = -(-N // 128)
+    keep = np.ones((2, nb, nb), bool)
+    q, k, v, dout, lam, rp, ci, *_ = make(1, N, 2, d, keep, 37, lam_type=torch.float32)
+    q[0, :, 0, 3], q[0, :, 1, d // 2 + 3] = 1.0, 1.0
+    k[0, [3, 6, 71, N - 1], 0, 3], k[0, [7, 130], 1, d // 2 + 3] = -math.inf, -math.inf
+    out, out2, lse = sl.diff_attn_forward_lse(q, k, v, rp, ci, lam)
+    got = sl.diff_attn_backward(q, k, v, out, out2, dout, lse, rp, ci, lam)
+    _, dk, dv, dlam, size, *_ = reference_gradients(q, k, v, dout, keep, lam, False)
+    for name, ref in (("dk", dk), ("dv", dv)):
+        for h in range(2):
+            other = torch.isfinite(k[0, :, h]).all(-1)
+            rows_ok(got[name][0, other, h], ref[0, other, h], name)
+    assert bool(((got["dlam"].double() - dlam).abs() <= 2.0 ** -24 * dlam.abs() + 1e-4 * size).all())
