@@ -232,11 +232,11 @@ __global__ void __launch_bounds__(kDiffThreads, 1)
       for (int j = 0; j < n; ++j) {
         const int s = j % C::STAGES, col = col_idx[c0 + j];
         const uint32_t ph = (uint32_t)((j / C::STAGES) & 1);
-        if (!mbar_await_one(&sh->k_empty[s], ph ^ 1, polls)) { ok = false; break; }
+        if (!mbar_await_one(&sh->k_empty[s], ph ^ 1, limit_ns)) { ok = false; break; }
         mbar_arrive_expect_tx(&sh->k_full[s], C::TILE);
         tma_load_4d(smem + C::OFF_K + s * C::TILE, &tm_k, &sh->k_full[s], 0, col * 128, h * C::DCH, b);
         ++kl;
-        if (!mbar_await_one(&sh->v_empty[s], ph ^ 1, polls)) { ok = false; break; }
+        if (!mbar_await_one(&sh->v_empty[s], ph ^ 1, limit_ns)) { ok = false; break; }
         mbar_arrive_expect_tx(&sh->v_full[s], C::TILE);
         tma_load_4d(smem + C::OFF_V + s * C::TILE, &tm_v, &sh->v_full[s], 0, col * 128, h * C::DCH, b);
         ++vl;

@@ -233,11 +233,11 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       // K_j is free once the gradient products of tile j have read it, V_j once dP_j is done
       for (int j = 0; j < n; ++j) {
         const int col = col_idx[c0 + j], ks = j % 3, vs = j & 1;
-        if (!mbar_await_one(&sh->k_empty[ks], (uint32_t)((j / 3) & 1) ^ 1, polls)) { ok = false; break; }
+        if (!mbar_await_one(&sh->k_empty[ks], (uint32_t)((j / 3) & 1) ^ 1, limit_ns)) { ok = false; break; }
         mbar_arrive_expect_tx(&sh->k_full[ks], C::TILE);
         tma_load_4d(smem + C::DQ_OFF_K + ks * C::TILE, &tm_k, &sh->k_full[ks], 0, col * 128, h * C::DCH, b);
         ++kl;
-        if (!mbar_await_one(&sh->v_empty[vs], (uint32_t)((j >> 1) & 1) ^ 1, polls)) { ok = false; break; }
+        if (!mbar_await_one(&sh->v_empty[vs], (uint32_t)((j >> 1) & 1) ^ 1, limit_ns)) { ok = false; break; }
         mbar_arrive_expect_tx(&sh->v_full[vs], C::TILE);
         tma_load_4d(smem + C::DQ_OFF_V + vs * C::TILE, &tm_v, &sh->v_full[vs], 0, col * 128, h * C::DCH, b);
         ++vl;
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
       for (int i = 0; i < 2 * n; ++i) {
         if ((i & 1) == 0) qi = t_col_idx[c0 + (i >> 1)];
         const int s = i % C::STAGES, q0 = qi * 128 + 64 * (i & 1);
-        if (!mbar_await_one(&sh->ring_empty[s], (uint32_t)((i / C::STAGES) & 1) ^ 1, polls)) {
+        if (!mbar_await_one(&sh->ring_empty[s], (uint32_t)((i / C::STAGES) & 1) ^ 1, limit_ns)) {
           ok = false;
           break;
         }
