@@ -576,6 +576,12 @@ def _ptr(t, dtype, name) -> int:
     return t.data_ptr()
 
 
+def _int32(name, *sizes):
+    """Refuses sizes that the C interface's int would silently cut."""
+    if max(sizes) > 0x7FFFFFFF:
+        raise SaladError(SALAD_ERR_UNSUPPORTED, f"{name}: sizes {sizes}")
+
+
 def _new_like(x, dtype):
     """Contiguous memory of x's shape."""
     return torch.empty_like(x, dtype=dtype, memory_format=torch.contiguous_format)
@@ -625,6 +631,7 @@ def _rope(q, k, inv_freq, sections, interleaved, scale, positions, grid, origin,
     if q.dim() != 4:
         raise ValueError("q and k must be [B, N, heads, d] with the same B, N and d")
     B, N, _, d = q.shape
+    _int32("salad_rope", *q.shape)
     kind = q.dtype
     if kind not in _TYPES or (out_dtype is not None and out_dtype not in _TYPES):
         raise TypeError("q, k and the outputs must be fp32, bf16 or fp16")
@@ -747,6 +754,7 @@ def _ckpt_call(fn, name, xs, cks, fmt, stream):
     for x, c in zip(xs, cks):
         if x.numel():
             rows, cols, stride = _rows_of(x)
+            _int32(name, rows, cols)
             groups.setdefault((rows, cols, x.dtype), []).append(
                 _CKPT_TENSOR(x.data_ptr(), stride, c.codes.data_ptr(), c.scales.data_ptr()))
     s = _stream(stream)
