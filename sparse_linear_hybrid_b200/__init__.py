@@ -748,19 +748,26 @@ def _rows_of(x):
     return rows, cols, stride
 
 
-def _ckpt_call(fn, name, xs, cks, fmt, stream):
-    """One launch for tensors of the same layout, else one each."""
+def _ckpt_call(fn, name, xs, cks, fmt, stream, packed_as=None):
+    """One launch for tensors of the same layout, else one each; a checkpoint is of
+    the format packed_as once its launch has been taken."""
     groups = {}
     for x, c in zip(xs, cks):
         if x.numel():
             rows, cols, stride = _rows_of(x)
             _int32(name, rows, cols)
             groups.setdefault((rows, cols, x.dtype), []).append(
-                _CKPT_TENSOR(x.data_ptr(), stride, c.codes.data_ptr(), c.scales.data_ptr()))
+                (_CKPT_TENSOR(x.data_ptr(), stride, c.codes.data_ptr(), c.scales.data_ptr()), c))
+        elif packed_as is not None:
+            c.fmt, c.dtype = packed_as, x.dtype
     s = _stream(stream)
-    for (rows, cols, dtype), packed in groups.items():
-        for i in range(0, len(packed), 4):
-            _check(fn(b"".join(packed[i:i + 4]), len(packed[i:i + 4]), rows, cols, _TYPES[dtype], _FORMATS[fmt], s), name)
+    for (rows, cols, dtype), parts in groups.items():
+        for i in range(0, len(parts), 4):
+            part = parts[i:i + 4]
+            _check(fn(b"".join([p for p, _ in part]), len(part), rows, cols, _TYPES[dtype], _FORMATS[fmt], s), name)
+            if packed_as is not None:
+                for _, c in part:
+                    c.fmt, c.dtype = packed_as, dtype
 
 
 def _ckpt_scales_shape(shape):
@@ -795,9 +802,8 @@ def ckpt_pack(x, fmt: str = "int8", out=None, stream=None):
                     raise ValueError("the checkpoint's memory has another shape")
                 _on(t, c.codes, c.scales)
                 _ptr(c.codes, torch.uint8, "codes"), _ptr(c.scales, torch.uint8, "scales")
-                c.fmt, c.dtype = fmt, t.dtype
             res.append(c)
-        _ckpt_call(lib().salad_ckpt_pack, "salad_ckpt_pack", xs, res, fmt, stream)
+        _ckpt_call(lib().salad_ckpt_pack, "salad_ckpt_pack", xs, res, fmt, stream, packed_as=fmt)
     return res if many else res[0]
 
 
