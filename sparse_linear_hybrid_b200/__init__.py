@@ -51,6 +51,7 @@ _ROPE_TENSOR = struct.Struct("PPi4x6q").pack
 _CKPT_TENSOR = struct.Struct("PqPP").pack
 _INT3 = struct.Struct("3i").pack
 _NULL = contextlib.nullcontext()
+_INT_MAX = 0x7FFFFFFF
 
 
 class SaladError(RuntimeError):
@@ -578,7 +579,7 @@ def _ptr(t, dtype, name) -> int:
 
 def _int32(name, *sizes):
     """Refuses sizes that the C interface's int would silently cut."""
-    if max(sizes) > 0x7FFFFFFF:
+    if max(sizes) > _INT_MAX:
         raise SaladError(SALAD_ERR_UNSUPPORTED, f"{name}: sizes {sizes}")
 
 
@@ -631,7 +632,8 @@ def _rope(q, k, inv_freq, sections, interleaved, scale, positions, grid, origin,
     if q.dim() != 4:
         raise ValueError("q and k must be [B, N, heads, d] with the same B, N and d")
     B, N, _, d = q.shape
-    _int32("salad_rope", *q.shape)
+    if q.numel() > _INT_MAX:
+        _int32("salad_rope", *q.shape)
     kind = q.dtype
     if kind not in _TYPES or (out_dtype is not None and out_dtype not in _TYPES):
         raise TypeError("q, k and the outputs must be fp32, bf16 or fp16")
@@ -751,27 +753,35 @@ def _rows_of(x):
 def _ckpt_call(fn, name, xs, cks, fmt, stream, packed_as=None):
     """One launch for tensors of the same layout, else one each; a checkpoint is of
     the format packed_as once its launch has been taken."""
-    groups = {}
+    groups, filled = {}, {}
     for x, c in zip(xs, cks):
         if x.numel():
             rows, cols, stride = _rows_of(x)
-            _int32(name, rows, cols)
-            groups.setdefault((rows, cols, x.dtype), []).append(
-                (_CKPT_TENSOR(x.data_ptr(), stride, c.codes.data_ptr(), c.scales.data_ptr()), c))
+            if x.numel() > _INT_MAX:
+                _int32(name, rows, cols)
+            key = (rows, cols, x.dtype)
+            groups.setdefault(key, []).append(_CKPT_TENSOR(x.data_ptr(), stride, c.codes.data_ptr(), c.scales.data_ptr()))
+            if packed_as is not None:
+                filled.setdefault(key, []).append(c)
         elif packed_as is not None:
             c.fmt, c.dtype = packed_as, x.dtype
     s = _stream(stream)
-    for (rows, cols, dtype), parts in groups.items():
-        for i in range(0, len(parts), 4):
-            part = parts[i:i + 4]
-            _check(fn(b"".join([p for p, _ in part]), len(part), rows, cols, _TYPES[dtype], _FORMATS[fmt], s), name)
-            if packed_as is not None:
-                for _, c in part:
+    for (rows, cols, dtype), packed in groups.items():
+        for i in range(0, len(packed), 4):
+            _check(fn(b"".join(packed[i:i + 4]), len(packed[i:i + 4]), rows, cols, _TYPES[dtype], _FORMATS[fmt], s), name)
+            if filled:
+                for c in filled[rows, cols, dtype][i:i + 4]:
                     c.fmt, c.dtype = packed_as, dtype
 
 
 def _ckpt_scales_shape(shape):
     return (*shape[:-1], (shape[-1] + 31) // 32)
+
+
+def _once(outs):
+    given = [id(c) for c in outs if c is not None]
+    if len(set(given)) < len(given):
+        raise ValueError("the same output is given twice")
 
 
 def ckpt_pack(x, fmt: str = "int8", out=None, stream=None):
@@ -787,6 +797,8 @@ def ckpt_pack(x, fmt: str = "int8", out=None, stream=None):
     outs = (None,) * len(xs) if out is None else out if many else (out,)
     if not xs or len(outs) != len(xs):
         raise ValueError("one output for each tensor")
+    if out is not None:
+        _once(outs)
     ctx, dev = _on(*xs)
     res = []
     with _at(ctx, dev, stream):
@@ -803,7 +815,7 @@ def ckpt_pack(x, fmt: str = "int8", out=None, stream=None):
                 _on(t, c.codes, c.scales)
                 _ptr(c.codes, torch.uint8, "codes"), _ptr(c.scales, torch.uint8, "scales")
             res.append(c)
-        _ckpt_call(lib().salad_ckpt_pack, "salad_ckpt_pack", xs, res, fmt, stream, packed_as=fmt)
+        _ckpt_call(lib().salad_ckpt_pack, "salad_ckpt_pack", xs, res, fmt, stream, None if out is None else fmt)
     return res if many else res[0]
 
 
@@ -815,6 +827,8 @@ def ckpt_unpack(ckpt, dtype=None, out=None, stream=None):
     outs = (None,) * len(cks) if out is None else out if many else (out,)
     if not cks or len(outs) != len(cks):
         raise ValueError("one output for each checkpoint")
+    if out is not None:
+        _once(outs)
     fmt = cks[0].fmt
     if fmt not in _FORMATS or any(c.fmt != fmt for c in cks):
         raise ValueError("the checkpoints have several formats")

@@ -29,3 +29,18 @@ def test_a_refused_call_leaves_a_checkpoint_as_it_was():
     assert again is c and (c.fmt, c.dtype) == ("e4m3", torch.float16)
     empty = sl.ckpt_pack(torch.empty(0, 64, device="cuda"))
     assert sl.ckpt_pack(torch.empty(0, 64, device="cuda").half(), fmt="e4m3", out=empty).fmt == "e4m3"
+
+
+def test_an_output_is_given_once():
+    """Of several layouts, or more tensors than a launch takes, each goes by itself: the library's own check of overlaps
+    does not see two of them."""
+    x = torch.randn(4, 33, device="cuda")
+    apart = torch.randn(4, 40, device="cuda")[:, :32]
+    c, a = sl.ckpt_pack(x), sl.ckpt_pack(x[:, :32].contiguous())
+    for xs, outs in (([x[:, :32].contiguous(), apart], [a, a]), ([x] * 5, [c, *sl.ckpt_pack([x] * 3), c])):
+        with pytest.raises(ValueError, match="twice"):
+            sl.ckpt_pack(xs, out=outs)
+    y = torch.empty_like(x)
+    with pytest.raises(ValueError, match="twice"):
+        sl.ckpt_unpack([c] * 5, out=[y, *(torch.empty_like(x) for _ in range(3)), y])
+    assert [s.fmt for s in sl.ckpt_pack([x, x], out=[None, c])] == ["int8", "int8"]
