@@ -354,14 +354,14 @@ def transpose_block_mask(row_ptr, col_idx, groups: int, nb: int, stream=None):
     return t_row_ptr, t_col_idx[:col_idx.numel()]
 
 
-def _transposed_mask(row_ptr, col_idx, t_row_ptr, t_col_idx, mask_per_bh, groups=0, nb=0):
-    """The transposed mask the backward walks for dk and dv: given, or the mask
-    itself for the symmetric window masks (rows per head), or built on the GPU
-    for a mask with rows per (b, h) (Top-K), which is not symmetric."""
+def _transposed_mask(row_ptr, col_idx, t_row_ptr, t_col_idx, build, groups=0, nb=0):
+    """The transposed mask the backward walks for dk and dv: given, or with `build`
+    built on the GPU (always for a mask with rows per (b, h), such as Top-K's, which
+    is not symmetric), or the mask itself, as for the symmetric window masks."""
     if (t_row_ptr is None) != (t_col_idx is None):
         raise ValueError("give both t_row_ptr and t_col_idx, or neither")
     if t_row_ptr is None:
-        if mask_per_bh:
+        if build:
             return transpose_block_mask(row_ptr, col_idx, groups, nb)
         return row_ptr, col_idx
     return t_row_ptr, t_col_idx
@@ -866,7 +866,9 @@ def attn_backward_ckpt(q, k, v, dout, row_ptr, col_idx, w_proj, gate, block: int
     """The whole layer's gradients from 8-bit checkpoints of q, k and v
     (ckpt_pack of [B, N, Hh, d] tensors): out and lse are computed again from the
     decoded values.  A dict of CUDA tensors: dq, dk, dv bf16 [B, N, Hh, d], dw fp32
-    [d, d], dgate fp32 [B, Hh]; the other arguments as attn_backward."""
+    [d, d], dgate fp32 [B, Hh]; the other arguments as attn_backward.  The transposed
+    mask is built on the GPU when none is given (about 20 us); a symmetric mask, such
+    as build_block_mask's, may be given as its own transpose."""
     if not (q.fmt == k.fmt == v.fmt) or not (q.codes.shape == k.codes.shape == v.codes.shape) or q.codes.dim() != 4:
         raise ValueError("checkpoints of q, k and v: one format, one shape [B, N, Hh, d]")
     B, N, Hh, d = q.codes.shape
@@ -881,8 +883,8 @@ def attn_backward_ckpt(q, k, v, dout, row_ptr, col_idx, w_proj, gate, block: int
         nb = (N + block - 1) // block
         if row_ptr.numel() != (B * Hh if mask_per_bh else Hh) * nb + 1:
             raise ValueError(f"row_ptr has {row_ptr.numel()} entries, not {(B * Hh if mask_per_bh else Hh) * nb + 1}")
-        t_row_ptr, t_col_idx = _transposed_mask(row_ptr, col_idx, t_row_ptr, t_col_idx,
-                                                mask_per_bh and col_idx.numel(), B * Hh, nb)
+        t_row_ptr, t_col_idx = _transposed_mask(row_ptr, col_idx, t_row_ptr, t_col_idx, col_idx.numel(),
+                                                B * Hh if mask_per_bh else Hh, nb)
         if t_row_ptr.shape != row_ptr.shape:
             raise ValueError("the transposed mask has another number of rows")
         res = {n: torch.empty(B, N, Hh, d, dtype=torch.bfloat16, device=dev) for n in ("dq", "dk", "dv")}
@@ -986,14 +988,17 @@ def diff_attn_backward(q, k, v, out, out2, dout, lse, row_ptr, col_idx, lam, t_r
                        softmax_scale: float = 0.0, mask_per_bh: bool = False, workspace=None, stream=None):
     """Gradients of differential attention (see salad_diff_backward): dict of dq, dk,
     dv bf16 [B, N, Hh, d] and dlam [Hh] of lam's type.  out, out2 and lse come from
-    diff_attn_forward_lse on the same inputs; the transposed mask as in attn_backward_sparse."""
+    diff_attn_forward_lse on the same inputs (with q, k, v decoded from a checkpoint: of
+    a forward on the decoded ones).  The transposed mask is built on the GPU when none
+    is given (about 20 us); a symmetric mask, such as build_block_mask's, may be given
+    as its own transpose."""
     ctx, dev = _on(q, k, v, out, out2, dout, lse, row_ptr, col_idx, lam,
                    *(t for t in (t_row_ptr, t_col_idx, workspace) if t is not None))
     with _at(ctx, dev, stream):
         B, N, Hh, d = q.shape
         _mask_rows(row_ptr, B, N, Hh, mask_per_bh)
-        t_row_ptr, t_col_idx = _transposed_mask(row_ptr, col_idx, t_row_ptr, t_col_idx,
-                                                mask_per_bh and col_idx.numel(), B * Hh, (N + 127) // 128)
+        t_row_ptr, t_col_idx = _transposed_mask(row_ptr, col_idx, t_row_ptr, t_col_idx, col_idx.numel(),
+                                                B * Hh if mask_per_bh else Hh, (N + 127) // 128)
         _mask_rows(t_row_ptr, B, N, Hh, mask_per_bh)
         if lse.shape != (2, B, Hh, N):
             raise ValueError(f"lse has shape {tuple(lse.shape)}, not {(2, B, Hh, N)}")

@@ -180,3 +180,22 @@ def test_gradients_beside_a_score_of_minus_infinity(N, d):
             other = torch.isfinite(k[0, :, h]).all(-1)
             rows_ok(got[name][0, other, h], ref[0, other, h], name)
     assert bool(((got["dlam"].double() - dlam).abs() <= 2.0 ** -24 * dlam.abs() + 1e-4 * size).all())
+
+
+def test_a_mask_that_is_not_symmetric():
+    """Rows per head, not symmetric, and no transposed mask given: the gradients are those with it."""
+    N, Hh, d = 300, 2, 64
+    keep = np.zeros((Hh, 3, 3), bool)
+    keep[0] = np.tril(np.ones((3, 3), bool))
+    keep[1, :, 1] = keep[1, 2, 0] = True
+    q, k, v, dout, lam, rp, ci, trp, tci = make(1, N, Hh, d, keep, 53)
+    out, out2, lse = sl.diff_attn_forward_lse(q, k, v, rp, ci, lam)
+    args = (q, k, v, out, out2, dout, lse, rp, ci, lam)
+    want = sl.diff_attn_backward(*args, t_row_ptr=trp, t_col_idx=tci)
+    got = sl.diff_attn_backward(*args)
+    assert all(torch.equal(got[n], want[n]) for n in want)
+    w, gate = (torch.randn(d, d, device="cuda") / 8).bfloat16(), torch.rand(1, Hh, device="cuda")
+    args = (*sl.ckpt_pack([q, k, v]), dout, rp, ci, w, gate)
+    want = sl.attn_backward_ckpt(*args, t_row_ptr=trp, t_col_idx=tci)
+    got = sl.attn_backward_ckpt(*args)
+    assert all(torch.equal(got[n], want[n]) for n in want)
