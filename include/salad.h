@@ -615,6 +615,9 @@ int salad_diff_forward(const void* q, const void* k, const void* v, int B, int N
  *   dq_1,i = scale sum_j ds_1,ij k_1,j,  dq_2,i = -lam scale sum_j ds_2,ij k_2,j,  dk_m,j likewise over i
  *   dv_j = sum_i (p_1 - lam p_2)_ij dout_i,   dlam[h] = -sum over b, i, j of p_2,ij dp_ij
  *   out, out2, lse  from salad_diff_forward with the same inputs; dout DEVICE bf16.
+ *                 (q, k, v decoded from a checkpoint: of a forward on the decoded
+ *                 ones.  With those of the originals p does not sum to 1, and the
+ *                 result is the gradient of no function.)
  *   t_row_ptr, t_col_idx  the transposed mask (as salad_attn_backward_sparse).
  *   dq, dk, dv  DEVICE bf16 [B][N][Hh][d], 16-byte aligned;  dlam DEVICE [Hh] of lam_type.
  * Sums are fp32 in a fixed order (deterministic), rounded once.  An infinite key

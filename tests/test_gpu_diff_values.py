@@ -199,3 +199,63 @@ def test_a_mask_that_is_not_symmetric():
     want = sl.attn_backward_ckpt(*args, t_row_ptr=trp, t_col_idx=tci)
     got = sl.attn_backward_ckpt(*args)
     assert all(torch.equal(got[n], want[n]) for n in want)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_gradients_at_decoded_values(fmt):
+    """A training step that keeps q, k and v in 8 bits: the backward gets the out, out2 and lse of a forward on the decoded
+    values, and gives the gradients at them."""
+    B, N, Hh, d = 2, 333, 2, 128
+    keep = np.random.default_rng(47).random((Hh, 3, 3)) < 0.7
+    keep[:, np.arange(3), np.arange(3)] = True
+    q, k, v, dout, lam, rp, ci, trp, tci = make(B, N, Hh, d, keep, 48, lam_type=torch.float32)
+    q, k, v = sl.ckpt_unpack(sl.ckpt_pack([q, k, v], fmt=fmt))
+    out, out2, lse = sl.diff_attn_forward_lse(q, k, v, rp, ci, lam)
+    got = sl.diff_attn_backward(q, k, v, out, out2, dout, lse, rp, ci, lam, t_row_ptr=trp, t_col_idx=tci)
+    dq, dk, dv, dlam, size, *_ = reference_gradients(q, k, v, dout, keep, lam, False)
+    for name, ref in (("dq", dq), ("dk", dk), ("dv", dv)):
+        rows_ok(got[name], ref, name)
+    assert bool(((got["dlam"].double() - dlam).abs() <= 2.0 ** -24 * dlam.abs() + 1e-4 * size).all())
+
+
+def test_training_step_with_8_bit_inputs():
+    """Rotation, forward, q, k and v kept in 8 bits; then decoded, forward again, gradients, rotation back: the gradients at
+    the decoded values, eager, and captured and replayed on new inputs."""
+    B, T, H, W, Hh, d = 1, 2, 9, 13, 2, 64
+    N, sections = T * H * W, (12, 10, 10)
+    keep = np.ones((Hh, 2, 2), bool)
+    q0, k0, v, dout, lam, *_ = make(B, N, Hh, d, keep, 59, lam_type=torch.float32)
+    rp, ci = sl.build_block_mask(T, H, W, 128, np.tile(np.int32([1, 8, 12]), (Hh, 1)))  # (every block: `keep`)
+    assert ci.numel() == keep.sum()
+    freq, scale = sl.rope_inv_freq(d, sections=sections)
+    kw = dict(sections=sections, interleaved=True, scale=scale, grid=(T, H, W))
+    ws = sl.new_diff_workspace(B, N, Hh, d)
+
+    def step():
+        q, k = sl.rope_forward(q0, k0, freq, **kw)
+        out = sl.diff_attn_forward(q, k, v, rp, ci, lam, workspace=ws)
+        kept = sl.ckpt_pack([q, k, v])
+        decoded = sl.ckpt_unpack(kept)
+        again = sl.diff_attn_forward_lse(*decoded, rp, ci, lam, workspace=ws)
+        grads = sl.diff_attn_backward(*decoded, *again[:2], dout, again[2], rp, ci, lam, t_row_ptr=rp, t_col_idx=ci, workspace=ws)
+        return [out, *decoded, *grads.values(), *sl.rope_backward(grads["dq"], grads["dk"], freq, **kw)]
+
+    def check(out, q, k, v8, dq, dk, dv, dlam, dq0, dk0):
+        check_forward(*sl.rope_forward(q0, k0, freq, **kw), v, keep, lam, out, None, None, False)
+        ref = reference_gradients(q, k, v8, dout, keep, lam, False)
+        for name, got, want in (("dq", dq, ref[0]), ("dk", dk, ref[1]), ("dv", dv, ref[2])):
+            rows_ok(got, want, name)
+        assert bool(((dlam.double() - ref[3]).abs() <= 2.0 ** -24 * ref[3].abs() + 1e-4 * ref[4]).all())
+        assert all(torch.equal(a, b) for a, b in zip((dq0, dk0), sl.rope_backward(dq, dk, freq, **kw)))
+
+    check(*step())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for t in (q0, k0, v, dout):
+        t.normal_()
+    graph.replay()
+    torch.cuda.synchronize()
+    check(*captured)
+    assert sl.check_status(ws) == sl.SALAD_OK
