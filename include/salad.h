@@ -516,7 +516,7 @@ typedef struct {
  * Angles are formed in fp64 and reduced before the fp32 sine and cosine; the
  * products are fp32 with one rounding to y's type.  Never synchronises, no
  * workspace.  Errors: INVALID_ARG, UNSUPPORTED (d > 512, more than 2^31 - 1
- * tokens), CUDA.
+ * tokens, more than 65,535 heads in all), CUDA.
  */
 int salad_rope(const salad_rope_tensor* tensors, int count, int x_type, int y_type, int B, int N, int d, int rot,
                int interleaved, const double* inv_freq, const int32_t* axis_pairs, int axes,
@@ -532,7 +532,9 @@ int salad_rope(const salad_rope_tensor* tensors, int count, int x_type, int y_ty
  *   e    = the smallest exponent >= -127 with max|x| / 2^e <= 127 (SALAD_INT8) or 448 (SALAD_E4M3)
  *   code = x / 2^e rounded to nearest even;  scale byte = e + 127;  decoded = code 2^e
  * An int8 code is off by at most half a step, 2^(e-1) <= max|x| / 127; an
- * e4m3 code by 2^-4 of the value, or 2^(e-10) near 0.  Decoding to bf16 is exact.
+ * e4m3 code by 2^-4 of the value, or 2^(e-10) near 0.  Decoding to bf16 is exact,
+ * but for e4m3 codes of fp32 groups below 2^-115: they may lie under bf16's smallest
+ * number (2^-133) and are rounded to its multiples.
  * A group that holds an infinity or a NaN decodes to NaN (byte 255).  A value
  * that would round past the output type's largest decodes to the largest.
  */
@@ -600,8 +602,8 @@ int salad_attn_backward_ckpt(const uint8_t* q_codes, const uint8_t* q_scales, co
  * products with fp32 accumulation, p rounded to bf16 for its product, fp32
  * softmax, one rounding of each output.  The sums hold p v with p up to 2^24:
  * |v| up to 2^88.  A row whose kept keys all score -inf is NaN, as by the
- * formula.  Never synchronises.  Errors:
- * INVALID_ARG, UNSUPPORTED (d, block, B*Hh*ceil(N/128) >= 2^24), WORKSPACE, CUDA.
+ * formula.  Never synchronises.  Errors: INVALID_ARG, UNSUPPORTED (d, block,
+ * N > 2^30, Hh > 65535, B*Hh*ceil(N/128) >= 2^24), WORKSPACE, CUDA.
  */
 size_t salad_diff_workspace_bytes(int B, int N, int num_heads, int d);
 int salad_diff_forward(const void* q, const void* k, const void* v, int B, int N, int num_heads, int d, int block,
@@ -639,7 +641,7 @@ int salad_diff_backward(const void* q, const void* k, const void* v, const void*
  *            Keys and values from lens[b] on are not read.
  * fp32 arithmetic, one rounding, a fixed order of sums; no workspace.  Meant
  * for one or two queries (the keys are read once per pair of them).  Errors:
- * INVALID_ARG, UNSUPPORTED (d, B*Hh*16 >= 2^31, Nq > 131070), CUDA.
+ * INVALID_ARG, UNSUPPORTED (d, B*Hh*16 >= 2^31, Nq > 131070, capacity > 2^30), CUDA.
  */
 int salad_diff_decode(const void* q, const void* k, const void* v, int B, int Nq, int capacity, int num_heads, int d,
                       const int32_t* lens, const void* lam, int lam_type, float softmax_scale, void* out,

@@ -821,7 +821,7 @@ def ckpt_pack(x, fmt: str = "int8", out=None, stream=None):
 
 def ckpt_unpack(ckpt, dtype=None, out=None, stream=None):
     """The values of a Checkpoint, or of each of a list, in `dtype` (by default the
-    packed tensor's); exact for bf16 and fp32."""
+    packed tensor's); exact for bf16 and fp32 (see salad.h for bf16's smallest)."""
     many = isinstance(ckpt, (list, tuple))
     cks = ckpt if many else (ckpt,)
     outs = (None,) * len(cks) if out is None else out if many else (out,)

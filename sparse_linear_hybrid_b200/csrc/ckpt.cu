@@ -4,7 +4,7 @@
 //   code = round to nearest even (x / 2^e),   decoded = code 2^e
 // Scales are powers of two, so x / 2^e is exact in fp32, the code depends on x
 // alone (not on the order or width of the arithmetic) and the decoded value has
-// at most 7 (int8) or 4 (e4m3) significant bits: exact in bf16.  A group that
+// at most 7 (int8) or 4 (e4m3) significant bits: exact in bf16 (from 2^-133 on).  A group that
 // holds an infinity or a NaN has the byte 255 and decodes to NaN.
 //
 // Bound by memory: 2 + 1 + 1/32 bytes a bf16 value each way (three tensors of 50 M
