@@ -27,12 +27,13 @@
 // (384 scores, 512 P V, at d = 128) and 768 of the special-function unit, with one
 // pair of exponentials in four on the FMA pipe (exp2_fma_x2; 32,760 tokens x 12
 // heads of 128 at 90 % block sparsity, taken in turn: none 983 us, one in eight 932,
-// one in four and three in eight 914, one in two 924), and takes 1,500 (1.59 M active
-// cycles an SM over 1,068 steps, the ends of a CTA included).  The watch over
-// the cubic's range (softmax_pass) added 7 us to that, 927 -> 935 us taken in turn
-// on another box; 1,070 in a long run beside other work (0.99 TFLOP of products:
-// 1,060 and 930 TFLOP/s).  Every barrier wait is bounded; on a time-out the
-// kernel records it and drains.
+// one in four and three in eight 914, one in two 924), and takes 1,570 (1.68 M active
+// cycles an SM over 1,068 steps, the ends of a CTA included; the row warps issue in
+// 52 % of the cycles).  Two things that a right row needs are in that: the watch over
+// the cubic's range (softmax_pass; 927 -> 935 us taken in turn) and the sum of the
+// rounded weights (987 -> 1,032).  In a long run, 1,115 us (0.99 TFLOP of products:
+// 890 TFLOP/s).  Every barrier wait is bounded; on a time-out the kernel records it and
+// drains.
 #include "internal.h"
 #include "ptx.cuh"
 

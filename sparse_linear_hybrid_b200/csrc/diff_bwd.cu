@@ -23,10 +23,11 @@
 //   diff_dlam_kernel  sums the shares of every head in a fixed order
 // Gradients are rounded once, to bf16 (dlam to lam's type).  P and dS enter their
 // products as bf16, a choice: half a step of each weight, averaged over the sum.
-// Of one 9,360-token step of 12 heads of 128 (forward and backward 949 to 1,025 us
-// a call by box) the prep takes 21 us, dQ 326, dK/dV 399, by themselves; the tensor cores are
+// Of one 9,360-token step of 12 heads of 128 (forward and backward 1,047 us, 1,091 in a
+// long run) the prep takes 22 us, dQ 327, dK/dV 395, by themselves; the tensor cores are
 // busy 45 and 49 % of that.  dK/dV is bound by shared memory (its products read
-// both operands from there, dS_2^T passes through it), dQ by the row warps.  One
+// both operands from there, dS_2^T passes through it), dQ by the row warps, the prep
+// by its instructions (it issues in 66 % of the cycles, at 49 % of DRAM's rate).  One
 // pair of exponentials in four on the FMA pipe (949 us; none 955, one in two 986).
 // Warp roles, 384 threads: warp 0 TMA producer, warps 1-3 tcgen05 issuers (warp 1 owns the tensor
 // memory), warps 4-11 the rows (TMEM lane quarter = warp % 4).  There are several

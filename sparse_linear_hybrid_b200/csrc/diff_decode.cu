@@ -3,10 +3,13 @@
 // the output is 0).
 //
 // Bound by memory: each live key and value is read once per query or pair of
-// queries (4 x 32,760 keys x 12 heads of 128, one query each: 138 us, 5.84 TB/s).
-// The keys of a (b, h) are split over the CTAs of a cluster (up to 16) so that a
-// short batch still fills the machine; every warp keeps an online softmax of its keys (running maxima, sums and weighted values of both maps in
-// fp32 registers, d/8 lanes a key, eight features a lane), the warps join in
+// queries (12 heads of 128, one query each: 4 x 32,760 keys 145 us, 5.6 TB/s;
+// 4 x 28,665 keys 128 us, 5.5 TB/s; lengths of 24,570 to 32,760 with that sum 133 us,
+// because the split goes by the cache's capacity and the CTAs of the longest sequence
+// have the most keys).  The keys of a (b, h) are split over the CTAs of a cluster (up
+// to 16) so that a short batch still fills the machine; every warp keeps an online
+// softmax of its keys (running maxima, sums and weighted values of both maps in fp32
+// registers, d/8 lanes a key, eight features a lane), the warps join in
 // shared memory and the cluster through distributed shared memory: one launch,
 // no workspace.  Lanes of a key's first half of features form the score of map
 // 1, the others that of map 2, and one exchange hands each the other's.
