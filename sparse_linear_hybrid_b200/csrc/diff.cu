@@ -34,8 +34,8 @@
 // rounded weights (987 -> 1,032).  In a long run, 1,115 us (0.99 TFLOP of products:
 // 890 TFLOP/s).  Every barrier wait is bounded; on a time-out the kernel records it and
 // drains.
+#include "diff.cuh"
 #include "internal.h"
-#include "ptx.cuh"
 
 namespace salad {
 namespace {
@@ -82,10 +82,6 @@ struct DiffCfg {
 __device__ __forceinline__ void diff_timeout(DiffShared* sh, uint32_t* status) {
   sh->abort_flag = 1;
   atomicOr(status, kStatusTimeout);
-}
-
-__device__ __forceinline__ float lambda_of(const void* lam, int bf16, int h) {
-  return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(lam)[h] << 16) : static_cast<const float*>(lam)[h];
 }
 
 // -inf in place of the scores from column `valid` on.

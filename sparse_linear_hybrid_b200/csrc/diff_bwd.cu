@@ -36,8 +36,8 @@
 // issuer two of the eight row warps ran 500 to 900 of 2,400 cycles a step behind
 // the others (clock64).  Every barrier wait is bounded; on a time-out the kernel
 // records it and drains.
+#include "diff.cuh"
 #include "internal.h"
-#include "ptx.cuh"
 
 namespace salad {
 namespace {
@@ -86,9 +86,6 @@ struct DiffBwdCfg {
 };
 
 __device__ __forceinline__ void diff_bwd_timeout(uint32_t* status) { atomicOr(status, kStatusTimeout); }
-__device__ __forceinline__ float diff_lambda(const void* lam, int bf16, int h) {
-  return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(lam)[h] << 16) : static_cast<const float*>(lam)[h];
-}
 
 // K-steps [first, first + count) of X Y^T into D, both K-major: 128-byte rows in
 // 64-feature chunks, X's of 128 rows, Y's of y_chunk bytes; the first one overwrites.
@@ -142,7 +139,7 @@ __global__ void __launch_bounds__(256)
     float* at = rows + bh * npad * 4 + n / 64 * 256 + n % 64;
     at[0] = n < N ? lse[bh * N + n] * kDiffLog2e : kDiffPadLse;
     at[64] = n < N ? lse[(BH + bh) * N + n] * kDiffLog2e : kDiffPadLse;
-    at[128] = fmaf(diff_lambda(lam, lam_bf16, h), d2, d0);
+    at[128] = fmaf(lambda_of(lam, lam_bf16, h), d2, d0);
     at[192] = d2;
   }
 }
@@ -372,7 +369,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     } else {
       tc_fence_after();
       const int row = qt * 128 + r;
-      const float mul = half ? -diff_lambda(lam, lam_bf16, h) * scale : scale;  // half: the map whose dq this thread writes
+      const float mul = half ? -lambda_of(lam, lam_bf16, h) * scale : scale;  // half: the map whose dq this thread writes
       uint16_t* dst = dq + (((size_t)b * N + row) * heads + h) * D + half * (D / 2);
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
@@ -540,7 +537,7 @@ __global__ void __launch_bounds__(kDiffBwdThreads, 1)
     // one thread a key row and half of a step's queries
     const int quarter = warp & 3, r = quarter * 32 + lane, half = (warp - 4) >> 2;
     const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
-    const float lh = diff_lambda(lam, lam_bf16, h);
+    const float lh = lambda_of(lam, lam_bf16, h);
     const uint64_t c2 = f32x2_pack(scale_log2, scale_log2), nlam = f32x2_pack(-lh, -lh);
     const uint64_t minus = f32x2_pack(-1.f, -1.f), zero = f32x2_pack(0.f, 0.f);
     bool ok = limit_ns != 0;

@@ -19,10 +19,6 @@ __device__ __forceinline__ uint32_t lane_id() {
   return l;
 }
 
-// A value that is the same in all lanes of a converged warp, told to the compiler
-// (it then keeps what follows from it in uniform registers and branches as a warp).
-__device__ __forceinline__ int warp_uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-
 __device__ __forceinline__ uint64_t global_timer_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
@@ -56,18 +52,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// The same without the machine's own wait: one look.
-__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // Bounded wait: polls until the phase completes or `limit_ns` of global time
 // has passed (limit 0: a single probe).  Returns false on time-out.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
@@ -88,47 +72,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
   const bool ok = mbar_wait(bar, parity, limit_ns);
   return __all_sync(0xffffffffu, ok);
-}
-
-// Bounded wait of a converged warp, lane by lane: after `polls` polls a lane's `ok` turns
-// false, and its later waits only look.  The polls behind the first do not block
-// (test_wait; try_wait held a thread for 4 us) and sleep 40 ns at most, so that each takes
-// 128 ns or less (64 measured) and their count keeps the limit in time; reading the timer
-// in their place cost the differential forward 2 to 6 %.  The caller
-// goes on with its loop, without a vote or a way out (either costs the compiler its
-// uniform branches: 1,051 against 955 us for the differential forward at 1.3B), but
-// a lane arrives, commits and issues nothing while its ok is false: a stage given
-// back before its copy has landed would let the CTA end with the copy in flight.
-// The caller votes on ok behind its loop.  With a limit of 0 (a test hook) ok is
-// false from the start.
-__device__ __forceinline__ uint32_t polls_of(uint64_t limit_ns) {
-  const uint64_t n = limit_ns / 128;
-  return n > 0x7FFFFFFFull ? 0x7FFFFFFFu : (uint32_t)n + 1u;
-}
-__device__ __forceinline__ void mbar_await(uint64_t* bar, uint32_t parity, uint32_t polls, bool& ok) {
-  if (!mbar_try_wait(bar, parity)) {
-    uint32_t left = ok ? polls : 1u;
-#pragma unroll 1
-    do {
-      if (--left == 0) {
-        ok = false;
-        break;
-      }
-      __nanosleep(20);
-    } while (!mbar_test_wait(bar, parity));
-  }
-  __syncwarp();
-}
-// Bounded wait of one thread that has time (a producer some stages ahead).
-__device__ __forceinline__ bool mbar_await_one(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
-  if (limit_ns == 0) return false;
-  const uint64_t t0 = global_timer_ns();
-  do {
-    __nanosleep(100);
-    if (mbar_test_wait(bar, parity)) return true;
-  } while (global_timer_ns() - t0 < limit_ns);
-  return false;
 }
 
 // ---------------------------------------------------------------- fences
@@ -195,17 +138,6 @@ __device__ __forceinline__ void bulk_wait_group_read0() {
 }
 
 // ---------------------------------------------------------------- tcgen05
-// True in one lane of a converged warp, always the same one.  An issuing warp
-// that runs its loop as a whole and branches on this only around the products
-// keeps their descriptors in uniform registers; a single thread that runs the
-// loop (lane == 0) moves them there for every product: 128 x 64 x 16 products
-// from tensor memory issue every 33 cycles this way and every 55 the other,
-// 16 alternating ones from shared and tensor memory in 1,040 against 1,980.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
-  return p != 0;
-}
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
                "r"(ncols)
@@ -365,13 +297,6 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return r;
 }
 
-// The same, NaN when one of them is.
-__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // Packed pairs of fp32 (sm_100 f32x2 arithmetic: two lanes per instruction).
 __device__ __forceinline__ uint64_t f32x2_pack(float lo, float hi) {
   uint64_t r;
@@ -384,11 +309,6 @@ __device__ __forceinline__ void f32x2_unpack(uint64_t v, float& lo, float& hi) {
 __device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {

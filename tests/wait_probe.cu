@@ -1,6 +1,6 @@
-// The bounded waits of csrc/ptx.cuh on barriers that nothing arrives at: one CTA of two
+// The bounded waits of csrc/diff.cuh on barriers that nothing arrives at: one CTA of two
 // warps, each wait with a limit.  Per wait: whether it was satisfied, and its time in ns.
-#include "ptx.cuh"
+#include "diff.cuh"
 
 __global__ void wait_probe(uint64_t limit_ns, uint64_t* out) {
   __shared__ uint64_t bar[2];
