@@ -19,6 +19,8 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import dataclasses
+import functools
+import inspect
 import math
 import os
 import struct
@@ -196,6 +198,22 @@ def _host_ptr(t: torch.Tensor, dtype, name: str) -> ctypes.c_void_p:
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _of_its_stream(fn):
+    """Makes a `stream` given to fn the current one: what the call allocates (outputs,
+    workspace, the transposed mask) and launches beside the library's kernels is then of
+    that stream, in order with them, and is not given out again while they use it."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
 _copy_streams = {}
 
 
@@ -219,6 +237,7 @@ def _build_csr(name, nb, heads, call, device):
     return row_ptr, col_idx[:int(nnz.value)]
 
 
+@_of_its_stream
 def build_block_mask(T: int, H: int, W: int, block: int, windows, device=None, stream=None):
     """ST-SWA block mask as a per-head CSR: (row_ptr, col_idx) int32 CUDA tensors."""
     win = np.ascontiguousarray(windows, dtype=np.int32).reshape(-1, 3)
@@ -248,6 +267,7 @@ def tile_num_blocks(T: int, H: int, W: int, tile) -> int:
     return nb.value
 
 
+@_of_its_stream
 def build_tile_mask(T: int, H: int, W: int, tile, windows, device=None, stream=None):
     """ST-SWA mask over bt x bh x bw boxes of the grid: per-head CSR (row_ptr, col_idx)."""
     bt, bh, bw = tile
@@ -274,6 +294,7 @@ def new_workspace(B: int, N: int, heads: int, d: int, device=None) -> torch.Tens
     return torch.zeros(workspace_bytes(B, N, heads, d), dtype=torch.uint8, device=device)
 
 
+@_of_its_stream
 def attn_forward(q, k, v, row_ptr, col_idx, w_proj, gate, block: int, softmax_scale: float = 0.0,
                  eps: float = 1e-6, out=None, workspace=None, stream=None, mask_per_bh: bool = False) -> torch.Tensor:
     """out = block-sparse attention + gate * (ReLU linear attention @ w_proj).
@@ -298,6 +319,7 @@ def attn_forward(q, k, v, row_ptr, col_idx, w_proj, gate, block: int, softmax_sc
     return out
 
 
+@_of_its_stream
 def attn_forward_lse(q, k, v, row_ptr, col_idx, w_proj, gate, block: int, softmax_scale: float = 0.0,
                      eps: float = 1e-6, out=None, lse=None, workspace=None, stream=None, mask_per_bh: bool = False):
     """attn_forward that also returns each row's log-sum-exp of the sparse softmax
@@ -319,6 +341,7 @@ def attn_forward_lse(q, k, v, row_ptr, col_idx, w_proj, gate, block: int, softma
     return out, lse
 
 
+@_of_its_stream
 def attn_forward_heads(q, k, v, head_begin: int, head_count: int, row_ptr, col_idx, w_proj, gate, block: int,
                        softmax_scale: float = 0.0, eps: float = 1e-6, out=None, workspace=None,
                        stream=None) -> torch.Tensor:
@@ -341,6 +364,7 @@ def attn_forward_heads(q, k, v, head_begin: int, head_count: int, row_ptr, col_i
     return out
 
 
+@_of_its_stream
 def transpose_block_mask(row_ptr, col_idx, groups: int, nb: int, stream=None):
     """The transposed mask on the GPU (salad_transpose_block_mask): for every
     group (head, or (b, h)) and key block J, the ascending query blocks whose
@@ -367,6 +391,7 @@ def _transposed_mask(row_ptr, col_idx, t_row_ptr, t_col_idx, build, groups=0, nb
     return t_row_ptr, t_col_idx
 
 
+@_of_its_stream
 def attn_backward_sparse(q, k, v, o, dout, lse, row_ptr, col_idx, block: int = 128, t_row_ptr=None,
                          t_col_idx=None, softmax_scale: float = 0.0, mask_per_bh: bool = False, workspace=None,
                          stream=None):
@@ -392,6 +417,7 @@ def attn_backward_sparse(q, k, v, o, dout, lse, row_ptr, col_idx, block: int = 1
     return tuple(grads)
 
 
+@_of_its_stream
 def attn_backward(q, k, v, out, dout, lse, row_ptr, col_idx, w_proj, gate, block: int = 128, t_row_ptr=None,
                   t_col_idx=None, softmax_scale: float = 0.0, eps: float = 1e-6, mask_per_bh: bool = False,
                   workspace=None, stream=None):
@@ -422,6 +448,7 @@ def attn_backward(q, k, v, out, dout, lse, row_ptr, col_idx, w_proj, gate, block
     return res
 
 
+@_of_its_stream
 def attn_forward_host(q, k, v, row_ptr, col_idx, w_proj, gate, block: int, out=None, staging=None,
                       heads_per_chunk: int = 0, softmax_scale: float = 0.0, eps: float = 1e-6, workspace=None,
                       stream=None, copy_streams=None, device=None):
@@ -457,6 +484,7 @@ def attn_forward_host(q, k, v, row_ptr, col_idx, w_proj, gate, block: int, out=N
     return out
 
 
+@_of_its_stream
 def attn_forward_tiles(q, k, v, grid, tile, row_ptr, col_idx, w_proj, gate, softmax_scale: float = 0.0,
                        eps: float = 1e-6, out=None, workspace=None, stream=None) -> torch.Tensor:
     """attn_forward with 3-D tile blocks: grid = (T, H, W), tile = (bt, bh, bw)
@@ -480,6 +508,7 @@ def attn_forward_tiles(q, k, v, grid, tile, row_ptr, col_idx, w_proj, gate, soft
     return out
 
 
+@_of_its_stream
 def gate_forward(q, t_emb, w_t, w_x, beta, threshold: float, gate_out=None, s_out=None, workspace=None,
                  stream=None) -> torch.Tensor:
     """Dynamic gate with branch dropping (see salad.h): fp32 [B, Hh] CUDA tensor,
@@ -503,6 +532,7 @@ def gate_forward(q, t_emb, w_t, w_x, beta, threshold: float, gate_out=None, s_ou
     return gate_out
 
 
+@_of_its_stream
 def build_topk_mask(q, k, block: int, keep: int, workspace=None, stream=None):
     """Top-K dynamic block mask (see salad.h) as a per-(b, h) CSR: (row_ptr,
     col_idx) int32 CUDA tensors, min(keep, nb) ascending key blocks per row."""
@@ -524,6 +554,7 @@ def build_topk_mask(q, k, block: int, keep: int, workspace=None, stream=None):
     return row_ptr, col_idx[:B * Hh * nb * kk]
 
 
+@_of_its_stream
 def attn_forward_static(q, k, v, row_ptr, col_idx, w_proj, gate, block: int, softmax_scale: float = 0.0,
                         eps: float = 1e-6, out=None, stream=None) -> torch.Tensor:
     """attn_forward for callers that cannot allocate device memory: the
@@ -1037,6 +1068,7 @@ def diff_attn_decode(q, k_cache, v_cache, lens, lam, softmax_scale: float = 0.0,
     return out
 
 
+@_of_its_stream
 def linear_state(k, v, gate=None, workspace=None, stream=None):
     """(S fp32 [B*Hh, d, d], z fp32 [B*Hh, d]) of the ReLU linear branch."""
     B, N, Hh, d = k.shape
